@@ -18,7 +18,7 @@ and head holds in order
             low nibble first
   K scales  [NG][P] pairs of fp16 (s, m): a code c stands for s c + m
   V codes   [P/16][4][16][D/64][4] 16-bit units: unit (tile, g, a, h, i) has
-            dims 64 h + 4 a + 0..3 of token 16 tile + 4 g + i
+            dims 64 h + a + 0, 16, 32, 48 of token 16 tile + 4 g + i
   V scales  [NG][P] pairs (s, m)
 Quantization of a group y: m = fp16(min y), s = fp16((max y - min y) / 15),
 code = clamp(round((y - m) (1 / s)), 0, 15), 0 where s is 0.
@@ -170,7 +170,7 @@ def _store(pages, P, D, G, page, slot, kq, ks, vq, vs):
     Kc, Ks, Vc, Vs = _places(pages, P, D, G)
     k = kq.to(torch.uint8).reshape(T, H, D // 32, 4, 4, 2).transpose(2, 3)
     Kc[page, :, slot] = k[..., 0] | (k[..., 1] << 4)
-    v = vq.to(torch.uint8).reshape(T, H, D // 64, 16, 2, 2).transpose(2, 3)
+    v = vq.to(torch.uint8).reshape(T, H, D // 64, 2, 2, 16).permute(0, 1, 5, 2, 3, 4)
     Vc[page, :, slot // 16, slot % 16 // 4, :, :, slot % 4] = v[..., 0] | (v[..., 1] << 4)
     Ks[page, :, :, slot] = ks
     Vs[page, :, :, slot] = vs
@@ -183,7 +183,7 @@ def _values(pages, P, D, G, page, slot):
     b = Kc[page, :, slot]                                              # [T, H, 4, D/32, 4]
     k = torch.stack((b & 15, b >> 4), -1).transpose(2, 3).reshape(T, H, D // G, G).float()
     b = Vc[page, :, slot // 16, slot % 16 // 4, :, :, slot % 4]        # [T, H, 16, D/64, 2]
-    v = torch.stack((b & 15, b >> 4), -1).transpose(2, 3).reshape(T, H, D // G, G).float()
+    v = torch.stack((b & 15, b >> 4), -1).permute(0, 1, 3, 4, 5, 2).reshape(T, H, D // G, G).float()
     ks, vs = Ks[page, :, :, slot].float(), Vs[page, :, :, slot].float()   # [T, H, NG, 2]
     k = k * ks[..., :1] + ks[..., 1:]
     v = v * vs[..., :1] + vs[..., 1:]
@@ -476,7 +476,7 @@ def exact(case, seed):
         code, scale, groups = P * D // 2, P * (D // case["group"]) * 4, D // case["group"]
         k = nibbles(raw[:, :code].reshape(-1, 4, D // 32, 4)).permute(0, 2, 1, 3).reshape(len(pages) * P, D)
         v = nibbles(raw[:, code + scale:2 * code + scale].reshape(-1, P // 16, 4, 16, D // 64, 4, 2))
-        v = v.permute(0, 1, 2, 5, 4, 3, 6).reshape(len(pages) * P, D)
+        v = v.permute(0, 1, 2, 5, 4, 6, 3).reshape(len(pages) * P, D)   # page, tile, g, i, h, dims / 16, a
         both = []
         for codes, at in ((k, code), (v, 2 * code + scale)):
             sm = raw[:, at:at + scale].contiguous().view(torch.float16).view(-1, groups, P, 2).to(d)

@@ -582,6 +582,194 @@ lt_status lt_compress_chunks_greedy(const uint8_t *src, const uint64_t *dst_off,
 lt_status lt_index_chunks(const uint8_t *comp, const uint64_t *comp_off, uint32_t n_chunks,
                           uint64_t *seq_off, uint32_t *seq_pos, uint64_t seq_cap, int threads);
 
+/*
+ * ---- operators on 4-bit memory ----
+ *
+ * What a serving step does with weights and a key/value cache that stay in
+ * 4 bits: products with the raw INT4 form of a weight, and a paged cache
+ * that is written, read and attended to without a dense copy.
+ *
+ * Element types of the dense side (activations, queries, keys, values).
+ */
+typedef enum lt_dtype { LT_F16 = 0, LT_BF16 = 1, LT_F32 = 2 } lt_dtype;
+
+/*
+ * lt_gemv_int4 -- y = x W^T for 1 to 64 vectors x, W never expanded:
+ *   y[b][r] = sum over c of x[b][c] * (q[r][c] - zp[g]) * scale[g]
+ * with packed, scales, zp, rows, cols and group as lt_dequant_int4.  The
+ * weight is not rounded to fp16 on the way (lt_dequant_int4's output is);
+ * products are exact in fp32, sums are fp32, in an order that depends on the
+ * sizes alone, and y is rounded once.  An infinite or NaN x[b][c] makes row b
+ * of y NaN or infinite.
+ *   x   DEVICE x_type (LT_F16 or LT_BF16) [batch][cols], rows x_stride
+ *       elements apart, aligned to its elements; 1 <= batch <= 64
+ *       (LT_ERR_UNSUPPORTED above)
+ *   y   DEVICE y_type [batch][rows], rows y_stride elements apart
+ * Any shape of lt_dequant_int4 is served; cols a multiple of 32 with groups
+ * of a multiple of 32 (or of whole rows), packed and the rows of x aligned to
+ * 16 bytes, are the fast ones.
+ */
+lt_status lt_gemv_int4(const uint8_t *packed, const uint16_t *scales, const int8_t *zp, uint64_t rows,
+                       uint64_t cols, uint64_t group, const void *x, uint64_t x_stride, uint32_t batch,
+                       lt_dtype x_type, void *y, uint64_t y_stride, lt_dtype y_type, void *stream);
+
+/*
+ * A key/value cache in 4 bits (HOST struct; pages is DEVICE memory).  Keys
+ * and values of page_tokens consecutive tokens of one sequence and one
+ * kv head share one block of lt_kv4_page_bytes; block h of page p starts at
+ * pages + (p * kv_heads + h) * lt_kv4_page_bytes.  Each token's head vector
+ * of head_dim values is quantized in groups of `group` consecutive values: a
+ * group has a scale s and an offset m in fp16, and a code c stands for
+ * s c + m.  With P = page_tokens, D = head_dim, NG = D / group a block holds
+ *   K codes   [P][4][D/32] dwords: dword (g, c) has values 32c + 8g + 0..7,
+ *             the first in the low nibble
+ *   K scales  [NG][P] dwords: s in the low half, m in the high half
+ *   V codes   [P/16][4][16][D/64][4] 16-bit units: unit (t, g, a, h, i) has
+ *             values 64h + a + 0, 16, 32, 48 of token 16t + 4g + i
+ *   V scales  [NG][P] dwords
+ * which are the orders in which the attention kernel's lanes take them.
+ *   page_tokens 32, 64, 128 or 256; head_dim 64, 128 or 256; group 32, 64,
+ *   128 or 256, at most head_dim (LT_ERR_UNSUPPORTED otherwise); pages
+ *   16-byte aligned
+ */
+typedef struct lt_kv4_cache {
+  uint8_t *pages;
+  uint64_t n_pages;
+  uint32_t page_tokens;
+  uint32_t kv_heads;
+  uint32_t head_dim;
+  uint32_t group;
+} lt_kv4_cache;
+
+/* Bytes of one page's block for one kv head; 0 for sizes that are not served. */
+uint64_t lt_kv4_page_bytes(uint32_t page_tokens, uint32_t head_dim, uint32_t group);
+
+/*
+ * The rows of one step (HOST struct; its members point to DEVICE memory).
+ * The step's n_tokens rows belong to n_seqs sequences: rows q_start[i] ..
+ * q_start[i+1] - 1 are the newest tokens of sequence i, whose cache holds
+ * kv_len[i] tokens with them.  With n = q_start[i+1] - q_start[i], row
+ * q_start[i] + j stands at position kv_len[i] - n + j, and position p lives
+ * in page page_table[i][p / page_tokens], slot p % page_tokens.
+ *   q_start     DEVICE int32[n_seqs + 1], from 0, non-decreasing
+ *   kv_len      DEVICE int32[n_seqs], >= 0
+ *   page_table  DEVICE int32[n_seqs][max_pages]; entries that no position
+ *               needs are not read
+ *   max_q_len, max_kv_len   upper bounds of what q_start and kv_len hold,
+ *               known on the host: rows of a sequence past max_q_len get no
+ *               attention; max_kv_len only steers how the work is split
+ * Rows outside every sequence (padding), and positions below 0, are left out.
+ */
+typedef struct lt_kv4_batch {
+  const int32_t *q_start;
+  const int32_t *kv_len;
+  const int32_t *page_table;
+  uint32_t n_seqs;
+  uint32_t max_pages;
+  uint32_t n_tokens;
+  uint32_t max_q_len;
+  uint32_t max_kv_len;
+} lt_kv4_batch;
+
+/*
+ * The new rows of a step (HOST struct; its pointers are DEVICE memory).
+ * Arrays of type `type` (LT_F16 or LT_BF16) are [n_tokens][heads][head_dim]
+ * with the last dimension contiguous, tokens and heads the given strides in
+ * elements apart (multiples of 8), 16-byte aligned.
+ *   k, v       the kv_heads keys and values
+ *   q, q_out   the `heads` queries beside them, and where they go after norm
+ *              and rotation; both NULL to leave queries out
+ *   q_norm,    type[head_dim] weights: y = x / sqrt(mean(x^2) + eps) * w for
+ *   k_norm     every head vector; NULL for no norm
+ *   cos, sin   float [rope_len][rotary_dim / 2], both or neither: values
+ *              (a, b) of a pair turn to (a cos - b sin, b cos + a sin) with
+ *              the row of the token's position; rotary_dim a multiple of 16
+ *              up to head_dim, the first rotary_dim values are turned, pairs
+ *              are (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ *              `neighbours` is not 0; 16-byte aligned
+ *   positions  int32[n_tokens] rows of cos and sin, or NULL: the tokens'
+ *              positions in their caches
+ */
+typedef struct lt_kv4_new {
+  const void *k;
+  const void *v;
+  const void *q;
+  void *q_out;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride;
+  const void *q_norm;
+  const void *k_norm;
+  const float *cos;
+  const float *sin;
+  const int32_t *positions;
+  uint32_t heads;
+  uint32_t rope_len;
+  uint32_t rotary_dim;
+  int32_t neighbours;
+  float eps;
+  lt_dtype type;
+} lt_kv4_new;
+
+/*
+ * lt_kv4_append -- the step's keys and values into the cache, the queries
+ * beside them: norm, rotation and quantization in one pass, all in fp32.
+ * A group y becomes m = fp16(min y), s = fp16((max y - min y) / 15), code =
+ * clamp(rne((y - m) * (1 / s)), 0, 15), 0 where s is 0; values beyond the
+ * range of fp16 are held at its ends, and a group with a NaN or an infinity
+ * stands for NaN throughout.
+ *   token_status  DEVICE int32[n_tokens] or NULL: LT_CHUNK_OK, or
+ *                 LT_CHUNK_BAD_TABLE for a token whose page id is outside
+ *                 [0, n_pages), whose position is past max_pages or whose
+ *                 rotation row is outside [0, rope_len): nothing of it is
+ *                 written to the cache, and its q_out is NaN
+ * Two rows of one call never share a slot as long as sequences do not share
+ * the pages that they append to.
+ */
+lt_status lt_kv4_append(const lt_kv4_cache *cache, const lt_kv4_batch *batch, const lt_kv4_new *rows,
+                        int32_t *token_status, void *stream);
+
+/*
+ * lt_kv4_read -- the values that the cache stands for at the step's rows (a
+ * batch whose q_start counts whole sequences reads whole sequences):
+ * s c + m, rounded once.
+ *   k, v          DEVICE type [n_tokens][kv_heads][head_dim], 16-byte
+ *                 aligned; either may be NULL
+ *   token_status  as lt_kv4_append; a bad token's values are NaN
+ */
+lt_status lt_kv4_read(const lt_kv4_cache *cache, const lt_kv4_batch *batch, void *k, void *v, lt_dtype type,
+                      int32_t *token_status, void *stream);
+
+/*
+ * lt_kv4_attention -- attention of the step's queries over the cache:
+ *   out[t][h] = sum_j w_j v_j,  w = softmax over the visible j of
+ *   scale * q[t][h] . k_j
+ * for kv head h / (heads / kv_heads).  A row at position p sees the
+ * positions j <= p, of these (window > 0) only j > p - window and j < sinks.
+ * A row that sees nothing gives 0.  A visible position whose page id is
+ * outside [0, n_pages) makes the row NaN; positions that a row does not see
+ * have no influence on it, whatever their slots hold.
+ *   q, out     DEVICE type (LT_F16 or LT_BF16) [n_tokens][heads][head_dim],
+ *              strides in elements (multiples of 8), 16-byte aligned;
+ *              heads a multiple of kv_heads
+ *   lse        DEVICE float [n_tokens][heads] or NULL: log of the sum of
+ *              exp(scale q . k_j) over the visible j (-inf where none)
+ *   workspace  DEVICE scratch of lt_kv4_attention_workspace_bytes, 16-byte
+ *              aligned, owned by the caller, needing no particular contents:
+ *              long caches are split over workgroups and joined from it in a
+ *              fixed order (results are the same bits on every call)
+ * Scores, softmax and sums are fp32.
+ */
+lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch, const void *q,
+                           int64_t q_token_stride, int64_t q_head_stride, uint32_t heads, lt_dtype type,
+                           float scale, uint32_t window, uint32_t sinks, void *out, int64_t out_token_stride,
+                           int64_t out_head_stride, float *lse, void *workspace, uint64_t workspace_bytes,
+                           void *stream);
+/* Bytes of workspace lt_kv4_attention needs (0: none, workspace may be NULL). */
+uint64_t lt_kv4_attention_workspace_bytes(const lt_kv4_cache *cache, const lt_kv4_batch *batch, uint32_t heads,
+                                          uint32_t window, uint32_t sinks);
+
 const char *lt_status_str(lt_status s);
 int lt_abi_version(void);
 

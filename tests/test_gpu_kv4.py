@@ -1,0 +1,503 @@
+"""The paged 4-bit key/value cache and attention over it against the 64-bit
+forms.
+
+Exact results: quantization of values that reach it unrounded (values, and
+keys without norm and rotation) repeats the stated fp32 steps bit for bit;
+reading back is one multiply-add in fp32 and one rounding.
+
+Tolerances.
+* Norm and rotation in fp32: the norm's sum over D squares, its root and two
+  products, the rotation's two products and a sum are at most D + 24 roundings
+  of 2^-24 of |a| + |b|, the pair's values (e below).  A stored value then
+  lies within half a step of its group, what rounding m and s to fp16 moves
+  (2^-11 of m and of 15 s), and e twice (of the value, and of the group's
+  ends).
+* Attention: a score is a sum of D products with codes and D / G with offsets
+  in fp32, with the scale: 2 D + 32 roundings of 2^-24 of |scale| sum |q||k|;
+  its exponential adds 2^-21.  Relative errors of that size in every weight
+  move the output by at most twice the weighted mean of |v - o|.  A weight
+  times a value's scale is rounded once to 11 bits: 2^-11 of the weighted mean
+  of the 8 steps that a code lies from the middle.  The output is rounded
+  once."""
+import numpy as np
+import pytest
+import torch
+
+import weight_dequantization_amd as lt
+from oracle import ops4
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+HALF = {F16: 2.0 ** -11, BF16: 2.0 ** -8}
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    yield
+    torch.cuda.synchronize()
+
+
+def i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(DEV)
+
+
+class Case:
+    """A cache with sequences of given lengths: random codes and scales where
+    tokens are, NaN and infinite scales everywhere else."""
+
+    def __init__(self, q_lens, kv_lens, P=32, H=2, D=128, G=64, pad=0, spare=2, seed=0):
+        self.P, self.H, self.D, self.G = P, H, D, G
+        self.q_lens, self.kv_lens = list(q_lens), list(kv_lens)
+        rng = self.rng = np.random.default_rng(seed + 13 * sum(kv_lens) + D)
+        need = [-(-k // P) for k in kv_lens]
+        n = sum(need) + spare
+        self.bytes = ops4.page_bytes(P, D, G)
+        pages = rng.integers(0, 256, (n, H, self.bytes)).astype(np.uint8)
+        self.table = np.full((len(kv_lens), max(need + [1]) + 1), -1, np.int64)
+        order = rng.permutation(n)
+        at = 0
+        for i, k in enumerate(need):
+            self.table[i, :k] = order[at:at + k]
+            at += k
+        sc = self.scales(pages)
+        for v in sc:                                        # whatever earlier owners left
+            v[..., 0] = rng.choice(np.array([0x7E00, 0x7C00, 0xFC00, 0x3C00], np.uint16), v.shape[:-1])
+            v[..., 1] = rng.choice(np.array([0x7E00, 0xFE00, 0x7C00, 0x0000], np.uint16), v.shape[:-1])
+        for i, k in enumerate(kv_lens):
+            for p in range(k):
+                for v in sc:
+                    s = rng.uniform(0.05, 0.4, (H, D // G)).astype(np.float16)
+                    m = (-7.5 * s + rng.uniform(-0.5, 0.5, s.shape)).astype(np.float16)
+                    v[self.table[i, p // P], :, :, p % P, 0] = s.view(np.uint16)
+                    v[self.table[i, p // P], :, :, p % P, 1] = m.view(np.uint16)
+        self.pages, self.T = pages, sum(q_lens) + pad
+        self.q_start = np.concatenate(([0], np.cumsum(q_lens)))
+
+    def scales(self, pages):
+        """Views [n, H, NG, P, 2] of the K and the V scales' bits."""
+        NG, n = self.D // self.G, pages.shape[0]
+        out = []
+        for is_v in (False, True):
+            a = ops4.scale_place(self.P, self.D, self.G, 0, 0, is_v)
+            out.append(pages[:, :, a:a + 4 * NG * self.P].view(np.uint16).reshape(n, self.H, NG, self.P, 2))
+            assert np.shares_memory(out[-1], pages)
+        return out
+
+    def device(self):
+        c = lt.Kv4Cache(torch.from_numpy(self.pages).to(DEV), self.P, self.H, self.D, self.G)
+        b = lt.Kv4Batch(i32(self.q_start), i32(self.kv_lens), i32(self.table), self.T, max(self.q_lens + [0]),
+                        max(self.kv_lens + [0]))
+        return c, b
+
+    def rows(self):
+        """(row, sequence, position) of every row that belongs to a sequence."""
+        for i, n in enumerate(self.q_lens):
+            for j in range(n):
+                yield int(self.q_start[i]) + j, i, self.kv_lens[i] - n + j
+
+    def seq(self, i, h, pages=None):
+        pages = self.pages if pages is None else pages
+        got = [ops4.get(pages[self.table[i, p // self.P], h], self.P, self.D, self.G, p % self.P)
+               for p in range(self.kv_lens[i])]
+        return [np.array(x).reshape(-1, self.D) for x in zip(*got)] if got else [np.zeros((0, self.D))] * 3
+
+
+def as_dtype(a, dtype):
+    return torch.from_numpy(np.asarray(a, np.float32)).to(dtype)
+
+
+# --------------------------------------------------------------------- read
+
+@pytest.mark.parametrize("D,G", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 64), (256, 128),
+                                 (256, 256)])
+@pytest.mark.parametrize("P,dtype", [(32, F16), (64, BF16), (256, F32)])
+def test_read_back_exact(D, G, P, dtype):
+    c = Case([5, 0, 40, 1], [5, 0, 70, 33], P=P, D=D, G=G, pad=2)
+    cache, batch = c.device()
+    st = torch.full((c.T,), -1, dtype=torch.int32, device=DEV)
+    k = torch.full((c.T, c.H, D), 5.0, dtype=dtype, device=DEV)
+    v = k.clone()
+    assert lt.kv4_read(cache, batch, k=k, v=v, status=st)[0] is k
+    for h in range(c.H):
+        whole = {i: c.seq(i, h) for i in range(4)}
+        for t, i, p in c.rows():
+            assert torch.equal(k[t, h].cpu(), as_dtype(whole[i][0][p], dtype)), (t, h)
+            assert torch.equal(v[t, h].cpu(), as_dtype(whole[i][1][p], dtype)), (t, h)
+    assert torch.all(k[-2:] == 5.0) and torch.all(v[-2:] == 5.0) and not st.any()
+
+
+def test_read_bad_pages_and_rows_before_the_start():
+    c = Case([3, 4], [40, 2], D=64, G=32)
+    c.table[0, 1] = c.pages.shape[0]
+    cache, batch = c.device()
+    st = torch.full((c.T,), -1, dtype=torch.int32, device=DEV)
+    k, v = torch.full((7, 2, 64), 5.0, device=DEV), torch.full((7, 2, 64), 5.0, device=DEV)
+    lt.kv4_read(cache, batch, k=k, v=v, status=st)
+    assert torch.isnan(k[:3]).all() and torch.isnan(v[:3]).all()
+    assert torch.all(k[3:5] == 5.0) and torch.isfinite(k[5:]).all()       # positions -2, -1, then 0, 1
+    assert st.tolist() == [lt.CHUNK_BAD_TABLE] * 3 + [0] * 4
+
+
+# ------------------------------------------------------------------- append
+
+def rope_table(n, r, seed=1):
+    a = np.random.default_rng(seed).uniform(0, 6.28, (n, r // 2))
+    return np.cos(a).astype(np.float32), np.sin(a).astype(np.float32)
+
+
+@pytest.mark.parametrize("D,G", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 64), (256, 256)])
+@pytest.mark.parametrize("P,dtype", [(32, F16), (128, BF16)])
+def test_append_values_bit_exact_and_nothing_else_written(D, G, P, dtype):
+    c = Case([5, 0, 37, 1, 3], [9, 4, 37, 66, 2], P=P, H=3, D=D, G=G, pad=1)
+    cache, batch = c.device()
+    k, v = (as_dtype(c.rng.standard_normal((c.T, 3, D)) * 2, dtype) for _ in range(2))
+    k[0, 0] = 1.5                                         # one value throughout
+    k[1, 0, :G] = float("nan")
+    v[1, 1, 3], v[2, 0, G - 1] = float("inf"), -float("inf")
+    v[3, 2] *= 1e-7 if dtype == F16 else 1e-30
+    if dtype == BF16:
+        k[2, 1] *= 1e9                                    # beyond fp16
+    ref = c.pages.copy()
+    for name, x, is_v in (("k", k, False), ("v", v, True)):
+        for t, i, p in c.rows():
+            if p >= 0:
+                codes, s, m = ops4.quantize(x[t].float().numpy(), G, np.float32)
+                for h in range(3):
+                    ops4.put(ref[c.table[i, p // P], h], P, D, G, p % P, codes[h], s[h], m[h], is_v)
+    st = torch.full((c.T,), -1, dtype=torch.int32, device=DEV)
+    assert lt.kv4_append(cache, batch, k.to(DEV), v.to(DEV), status=st) is None
+    got = cache.pages.cpu().numpy()
+    bad = np.nonzero(got != ref)
+    assert bad[0].size == 0, [b[:5] for b in bad]
+    assert not st.any()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,G,rotary,neighbours,normed", [
+    (64, 32, 64, False, True), (64, 64, 32, True, True), (128, 64, 128, False, True), (128, 128, 48, False, False),
+    (128, 32, 128, True, False), (128, 64, 16, True, True), (256, 64, 256, False, True), (256, 256, 0, False, True),
+    (256, 32, 80, True, True)])
+def test_append_norm_and_rotation(dtype, D, G, rotary, neighbours, normed):
+    c = Case([4, 1, 21], [4, 50, 30], H=2, D=D, G=G, seed=3)
+    cache, batch = c.device()
+    hq, eps = 6, 1e-5
+    # one projection's rows, sliced: heads D apart, tokens the whole row
+    qkv = as_dtype(c.rng.standard_normal((c.T, hq + 4, D)) * 3, dtype)
+    qw, kw = (as_dtype(c.rng.uniform(0.5, 1.5, D), dtype) for _ in range(2))
+    cos, sin = rope_table(64, rotary) if rotary else (None, None)
+    pos = c.rng.integers(0, 64, c.T) if neighbours else None
+    d = qkv.to(DEV)
+    q_out = lt.kv4_append(cache, batch, d[:, hq:hq + 2], d[:, hq + 2:], q=d[:, :hq],
+                          q_norm=qw.to(DEV) if normed else None, k_norm=kw.to(DEV) if normed else None, eps=eps,
+                          cos=None if cos is None else torch.from_numpy(cos).to(DEV),
+                          sin=None if sin is None else torch.from_numpy(sin).to(DEV), neighbours=neighbours,
+                          positions=None if pos is None else i32(pos))
+    got = cache.pages.cpu().numpy()
+    x = qkv.double().numpy()
+    for t, i, p in c.rows():
+        r = p if pos is None else pos[t]
+        for first, n, w in ((0, hq, qw), (hq, 2, kw)):
+            y = x[t, first:first + n]
+            if normed:
+                y = ops4.norm(y, w.double().numpy(), eps)
+            size = np.abs(y)
+            if rotary:
+                cs, sn = cos[r].astype(np.float64), sin[r].astype(np.float64)
+                size = size.copy()
+                a, b = ((slice(0, rotary, 2), slice(1, rotary, 2)) if neighbours else
+                        (slice(0, rotary // 2), slice(rotary // 2, rotary)))
+                size[:, a] = size[:, b] = size[:, a] + size[:, b]
+                y = ops4.rotate(y, cs, sn, neighbours)
+            e = (D + 24) * U * size
+            if first == 0:
+                off = np.abs(q_out[t].double().cpu().numpy() - y)
+                assert np.all(off <= e + HALF[dtype] * (np.abs(y) + e) + 2.0 ** -25), (t, off.max())
+                continue
+            for h in range(2):
+                k, _, _ = ops4.get(got[c.table[i, p // c.P], h], c.P, D, G, p % c.P)
+                g = y[h].reshape(-1, G)
+                lo, step = np.abs(g.min(1)), (g.max(1) - g.min(1)) / 15
+                tol = step / 2 * (1 + 2.0 ** -9) + 2.0 ** -11 * (lo + 15 * step) + 2.0 ** -23 + 2 * e[h].reshape(-1, G).max(1)
+                assert np.all(np.abs(k - y[h]) <= np.repeat(tol, G)), (t, h)
+
+
+def test_append_bad_tokens_are_left_out():
+    c = Case([2, 3, 2], [40, 3, 200], H=1, D=64, G=32, P=32)
+    c.table = c.table[:, :4].copy()          # positions 198, 199 have no entry
+    c.table[0, 1] = -7
+    cache, batch = c.device()
+    before = cache.pages.clone()
+    k = torch.randn(c.T, 1, 64, device=DEV).half()
+    q = torch.randn(c.T, 2, 64, device=DEV).half()
+    cos, sin = (torch.from_numpy(a).to(DEV) for a in rope_table(50, 64))
+    pos = i32([0, 0, 50, 3, -1, 0, 0])
+    st = torch.full((c.T,), -1, dtype=torch.int32, device=DEV)
+    q_out = lt.kv4_append(cache, batch, k, k, q=q, cos=cos, sin=sin, positions=pos, status=st)
+    bad = [0, 1, 2, 4, 5, 6]
+    assert st.tolist() == [lt.CHUNK_BAD_TABLE if t in bad else 0 for t in range(7)]
+    assert torch.isnan(q_out[bad]).all() and torch.isfinite(q_out[3]).all()
+    changed = (cache.pages != before).nonzero()[:, 0].unique().tolist()
+    assert changed == [int(c.table[1, 0])]
+
+
+def test_append_in_steps_equals_append_at_once():
+    D, G, P, T = 128, 64, 32, 75
+    k, v = (torch.randn(T, 2, D, device=DEV).half() for _ in range(2))
+    pages = [lt.Kv4Cache.empty(4, P, 2, D, G) for _ in range(2)]
+    table = i32([[2, 0, 3]])
+    lt.kv4_append(pages[0], lt.Kv4Batch(i32([0, T]), i32([T]), table, T, T, T), k, v)
+    at = 0
+    for n in (1, 2, 30, 1, 1, 17, 23):
+        lt.kv4_append(pages[1], lt.Kv4Batch(i32([0, n]), i32([at + n]), table, n, n, T), k[at:at + n], v[at:at + n])
+        at += n
+    whole = lt.Kv4Batch(i32([0, T]), i32([T]), table, T, T, T)
+    for a, b in zip(lt.kv4_read(pages[0], whole, dtype=F32), lt.kv4_read(pages[1], whole, dtype=F32)):
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- attention
+
+def run_attention(c, dtype, heads, window=0, sinks=0, scale=None, q=None, **kw):
+    cache, batch = c.device()
+    if q is None:
+        q = as_dtype(c.rng.standard_normal((c.T, heads, c.D)), dtype).to(DEV)
+    lse = torch.full((c.T, heads), 9.0, device=DEV)
+    out = lt.kv4_attention(cache, batch, q, scale=scale, window=window, sinks=sinks, lse=lse, **kw)
+    return q, out, lse
+
+
+def check_attention(c, dtype, heads, q, out, lse, window=0, sinks=0, scale=None, rows=None):
+    scale = c.D ** -0.5 if scale is None else scale
+    qd, od, ld = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    ratio, worst = heads // c.H, 0.0
+    for h in range(c.H):
+        seqs = {}
+        for t, i, p in c.rows():
+            if rows is not None and t not in rows:
+                continue
+            if i not in seqs:
+                seqs = {i: c.seq(i, h)}
+            for r in range(ratio):
+                hd = h * ratio + r
+                o, l, (wv, xs) = ops4.attention(qd[t, hd], *seqs[i], scale, p, window, sinks)
+                rel = (2 * c.D + 32) * U
+                tol = (2 * (rel * xs + 2.0 ** -21 * (wv + np.abs(o))) + 2.0 ** -11 * wv)
+                tol += HALF[dtype] * (np.abs(o) + tol) + 2.0 ** -25
+                off = np.abs(od[t, hd] - o)
+                assert np.all(off <= tol), (t, hd, p, float((off / tol).max()))
+                worst = max(worst, float((off / tol).max()))
+                if np.isinf(l):
+                    assert ld[t, hd] == l
+                else:
+                    size = scale if scale >= 0 else -scale
+                    size *= (np.abs(seqs[i][0]) @ np.abs(qd[t, hd])).max()
+                    assert abs(ld[t, hd] - l) <= rel * size + 2.0 ** -20 * (1 + abs(l)), (t, hd)
+    return worst
+
+
+LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 47, 63, 64, 65, 95, 96, 127, 128, 129, 200]
+
+
+@pytest.mark.parametrize("D,G,P,heads,H,dtype", [
+    (64, 32, 32, 2, 2, F16), (64, 64, 64, 6, 2, BF16), (128, 32, 64, 8, 1, F16), (128, 64, 64, 16, 2, F16),
+    (128, 128, 128, 4, 4, BF16), (256, 32, 32, 3, 1, BF16), (256, 64, 32, 10, 2, F16), (256, 128, 256, 2, 1, F16),
+    (256, 256, 32, 2, 1, F16)])
+def test_single_tokens(D, G, P, heads, H, dtype):
+    c = Case([1] * len(LENGTHS), LENGTHS, P=P, H=H, D=D, G=G)
+    check_attention(c, dtype, heads, *run_attention(c, dtype, heads))
+
+
+@pytest.mark.parametrize("heads,H", [(16, 1), (17, 1), (32, 1), (40, 1), (5, 5), (48, 3)])
+def test_head_ratios(heads, H):
+    c = Case([1, 2, 1], [70, 33, 1], H=H)
+    check_attention(c, F16, heads, *run_attention(c, F16, heads))
+
+
+@pytest.mark.parametrize("D,G,heads,H,dtype", [(64, 32, 4, 2, F16), (128, 64, 8, 2, BF16), (128, 128, 2, 2, F16),
+                                               (256, 64, 4, 1, F16)])
+def test_chunks_of_rows(D, G, heads, H, dtype):
+    """Several new tokens a sequence: none, all of it, behind a prefix; rows before the start see nothing."""
+    c = Case([7, 0, 33, 1, 70, 5], [7, 40, 130, 64, 99, 3], H=H, D=D, G=G, pad=3)
+    q, out, lse = run_attention(c, dtype, heads)
+    check_attention(c, dtype, heads, q, out, lse)
+    first = int(c.q_start[5])                       # 5 rows over 3 tokens: positions -2, -1
+    assert not out[first:first + 2].any() and torch.all(lse[first:first + 2] == -float("inf"))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 0), (33, 4), (64, 70), (1000, 4), (7, 1000)])
+@pytest.mark.parametrize("D,G,heads", [(64, 32, 6), (128, 64, 4)])
+def test_window_and_first_tokens(window, sinks, D, G, heads):
+    c = Case([1, 4, 40, 3, 1], [150, 77, 90, 2, 300], D=D, G=G)
+    q, out, lse = run_attention(c, F16, heads, window, sinks)
+    check_attention(c, F16, heads, q, out, lse, window, sinks)
+
+
+def test_long_caches_are_split_and_joined():
+    c = Case([1, 2, 1, 1], [5003, 2100, 9000, 3], P=64, H=1, D=64, G=64)
+    q, out, lse = run_attention(c, F16, 4)
+    check_attention(c, F16, 4, q, out, lse)
+    q, out, lse = run_attention(c, F16, 4, 3000, 5)
+    check_attention(c, F16, 4, q, out, lse, 3000, 5)
+
+
+def test_long_chunk_over_a_long_prefix():
+    c = Case([150, 20], [3100, 20], P=64, H=1, D=64, G=32)
+    q, out, lse = run_attention(c, BF16, 2)
+    check_attention(c, BF16, 2, q, out, lse, rows=set(range(0, 170, 7)))
+
+
+def test_empty_sequences():
+    c = Case([1, 2, 0], [0, 0, 0])
+    q, out, lse = run_attention(c, F16, 2)
+    assert not out.any() and torch.all(lse == -float("inf"))
+
+
+def test_padding_rows_and_rows_past_the_bound_are_left_alone():
+    c = Case([2, 3], [40, 9], pad=4)
+    cache, batch = c.device()
+    q = torch.randn(c.T, 2, 128, device=DEV).half()
+    out = torch.full_like(q, 3.0)
+    lt.kv4_attention(cache, batch, q, out=out)
+    assert torch.all(out[5:] == 3.0) and torch.isfinite(out).all() and not torch.any((out[:5] == 3.0).all(-1))
+    batch.max_q_len = 2
+    out = torch.full_like(q, 3.0)
+    lt.kv4_attention(cache, batch, q, out=out)
+    assert torch.all(out[4:] == 3.0) and not torch.any((out[:4] == 3.0).all(-1))
+
+
+def test_a_low_bound_of_the_lengths_changes_nothing_but_the_split():
+    c = Case([1, 1], [3000, 70], H=1, D=64, G=64)
+    q, out, lse = run_attention(c, F16, 2)
+    cache, batch = c.device()
+    batch.max_kv_len = 1
+    check_attention(c, F16, 2, q, lt.kv4_attention(cache, batch, q), lse)
+
+
+def test_bad_page_makes_its_rows_nan_and_no_others():
+    c = Case([40, 1, 1], [70, 40, 3000], H=2)
+    good = Case([40, 1, 1], [70, 40, 3000], H=2)
+    c.table[0, 1], c.table[2, 5] = 1 << 20, -3
+    q, out, lse = run_attention(c, F16, 4)
+    bad = [t for t, i, p in c.rows() if (i == 0 and p >= 32) or i == 2]
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    check_attention(good, F16, 4, q, out, lse, rows=set(range(c.T)) - set(bad))
+    # a window that does not reach the page leaves the row whole
+    q, out, lse = run_attention(c, F16, 4, 300, 2)
+    check_attention(good, F16, 4, q, out, lse, 300, 2, rows={c.T - 1})
+    # entries past the table's width are pages that are not there
+    c = Case([1], [70])
+    c.table = c.table[:, :2].copy()
+    assert torch.isnan(run_attention(c, F16, 2)[1]).all()
+
+
+def test_not_finite_tokens_reach_only_the_rows_that_see_them():
+    c = Case([40], [40], H=1, D=64, G=32, seed=8)
+    clean = c.pages.copy()
+    ks, vs = c.scales(c.pages)
+    ks[c.table[0, 0], 0, 1, 20, 1] = 0x7E00           # position 20: a NaN key, position 35: an infinite value
+    vs[c.table[0, 1], 0, 0, 3, 0] = 0x7C00
+    q, out, lse = run_attention(c, F16, 2)
+    assert torch.isnan(out[20:]).all() and torch.isfinite(out[:20]).all()
+    c.pages = clean
+    check_attention(c, F16, 2, q, out, lse, rows=set(range(20)))
+
+
+def test_not_finite_and_extreme_queries():
+    c = Case([6], [60], H=1, D=128, G=64)
+    q = as_dtype(c.rng.standard_normal((6, 2, 128)), BF16)
+    q[1, 0, 5], q[2, 1, 9], q[3] = float("nan"), float("inf"), 0.0
+    q[4] *= 1e-30
+    q[5, 0] *= 50.0                                     # one key takes all
+    q, out, lse = run_attention(c, BF16, 2, q=q.to(DEV))
+    assert torch.isnan(out[1, 0]).all() and torch.isnan(out[2, 1]).all()
+    check_attention(c, BF16, 2, q, out, lse, rows={0, 3, 4, 5})
+    assert torch.isfinite(out[1, 1]).all() and torch.isfinite(out[2, 0]).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_scales(scale):
+    c = Case([3, 1], [50, 33], H=1)
+    q, out, lse = run_attention(c, F16, 3, scale=scale)
+    check_attention(c, F16, 3, q, out, lse, scale=scale)
+
+
+def test_value_scales_of_very_different_size():
+    """Scales from fp16's smallest to thousands in one row, and groups of one value (scale 0)."""
+    c = Case([1, 1], [140, 40], H=1, D=64, G=32)
+    _, vs = c.scales(c.pages)
+    for i, n in ((0, 140), (1, 40)):
+        for p in range(n):
+            s = np.array([2.0 ** -24, 0.0, 3e-4, 1.0, 4000.0][p % 5 if i == 0 else p % 2], np.float16)
+            vs[c.table[i, p // 32], 0, :, p % 32, 0] = s.view(np.uint16)
+            vs[c.table[i, p // 32], 0, :, p % 32, 1] = np.float16(-7.5 * float(s) + 0.01).view(np.uint16)
+    q, out, lse = run_attention(c, F16, 3)
+    check_attention(c, F16, 3, q, out, lse)
+
+
+def test_strided_queries_and_outputs_and_side_stream():
+    c = Case([1, 9], [33, 70], D=64, G=64)
+    cache, batch = c.device()
+    wide = as_dtype(c.rng.standard_normal((c.T, 7, 3 * 64)), F16).to(DEV)
+    q = wide[:, 1:5, 64:128]
+    out = torch.full((4, c.T, 2 * 64), 7.0, dtype=F16, device=DEV)
+    lse = torch.zeros(c.T, 4, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    lt.kv4_attention(cache, batch, q, out=out.transpose(0, 1)[..., :64], lse=lse, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    check_attention(c, F16, 4, q, out.transpose(0, 1)[..., :64], lse)
+    assert torch.all(out[..., 64:] == 7.0)
+
+
+def test_same_bits_twice_and_in_a_replayed_graph():
+    """append, attention and a product captured once and replayed on new inputs, against the eager calls."""
+    c = Case([1, 1, 1], [3000, 64, 33], H=2, D=128, G=64, P=64)
+    cache, batch = c.device()
+    cos, sin = (torch.from_numpy(a).to(DEV) for a in rope_table(3000, 128))
+    w = torch.randint(0, 256, (512 * 512 // 2,), dtype=torch.uint8, device=DEV)
+    sc = torch.rand(512 * 512 // 128, device=DEV).half()
+    qkv = torch.empty(3, 8, 128, dtype=F16, device=DEV)
+    ws = torch.empty(max(lt.kv4_attention_workspace_bytes(cache, batch, 4), 16), dtype=torch.uint8, device=DEV)
+
+    def step(stream=None):
+        q = lt.kv4_append(cache, batch, qkv[:, 4:6], qkv[:, 6:], q=qkv[:, :4], cos=cos, sin=sin)
+        o = lt.kv4_attention(cache, batch, q, workspace=ws)
+        return o, lt.gemv_int4(w, sc, None, (512, 512), 128, o.view(3, 512))
+
+    qkv.normal_()
+    a, b = step(), step()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = step()
+    for _ in range(4):
+        qkv.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in held]
+        for x, y in zip(got, step()):
+            assert torch.equal(x, y)
+        torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """Pages whose block lies more than 4 GiB into the cache."""
+    D, G, P, H = 128, 64, 256, 8
+    per = ops4.page_bytes(P, D, G) * H
+    n = (5 << 30) // per
+    cache = lt.Kv4Cache.empty(n, P, H, D, G)
+    k, v = (torch.randn(3, H, D, device=DEV).half() for _ in range(2))
+    far, near = (lt.Kv4Batch(i32([0, 3]), i32([3]), i32([[page]]), 3, 3, 3) for page in (n - 1, 0))
+    q = torch.randn(3, H, D, device=DEV).half()
+    outs = []
+    for b in (far, near):
+        lt.kv4_append(cache, b, k, v)
+        outs.append((*lt.kv4_read(cache, b, dtype=F32), lt.kv4_attention(cache, b, q)))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.all((outs[0][0] - k).abs() < 0.3)

@@ -30,6 +30,14 @@ with the decode on a second stream):
     stream_fused_lz4_int4(host_table, scales, zp, shape, group, out=None, ...)
     stream_fused_lz4_int4_static(host_table, scales, zp, shape, group, out, ...)
         (the same with the library's static workspace: allocates nothing)
+Operators on 4-bit memory (products with raw INT4 weights, a paged key/value
+cache that stays in 4 bits):
+    gemv_int4(packed, scales, zp, shape, group, x) -> y = x W^T, 1 to 64 vectors
+    Kv4Cache(pages, page_tokens, kv_heads, head_dim, group), Kv4Cache.empty(...)
+    Kv4Batch(q_start, kv_len, page_table, n_tokens, max_q_len, max_kv_len)
+    kv4_append(cache, batch, k, v, q=None, ...) -> q after norm and rotation
+    kv4_read(cache, batch, dtype) -> (k, v)
+    kv4_attention(cache, batch, q, scale=None, window=0, sinks=0) -> out
 Host packer (numpy in, numpy out):
     pack_int4(codes) -> packed bytes (low nibble first)
     compress_chunks(src, dst_off, threads=0, max_dist=0) -> (comp, comp_off)
@@ -87,7 +95,30 @@ class _ZrTensor(C.Structure):
                 ("n_elem", C.c_uint64), ("n_vals", C.c_uint64)]
 
 
+class _Kv4Cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("n_pages", C.c_uint64), ("page_tokens", C.c_uint32),
+                ("kv_heads", C.c_uint32), ("head_dim", C.c_uint32), ("group", C.c_uint32)]
+
+
+class _Kv4Batch(C.Structure):
+    _fields_ = [("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p),
+                ("n_seqs", C.c_uint32), ("max_pages", C.c_uint32), ("n_tokens", C.c_uint32),
+                ("max_q_len", C.c_uint32), ("max_kv_len", C.c_uint32)]
+
+
+class _Kv4New(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("q", C.c_void_p), ("q_out", C.c_void_p),
+                ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64),
+                ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("q_out_token_stride", C.c_int64), ("q_out_head_stride", C.c_int64),
+                ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("cos", C.c_void_p), ("sin", C.c_void_p),
+                ("positions", C.c_void_p), ("heads", C.c_uint32), ("rope_len", C.c_uint32),
+                ("rotary_dim", C.c_uint32), ("neighbours", C.c_int32), ("eps", C.c_float), ("type", C.c_int32)]
+
+
 ZR_BLOCK = 1024          # LT_ZR_BLOCK
+F16, BF16, F32 = range(3)   # lt_dtype
 
 _L = None
 
@@ -101,6 +132,7 @@ def _lib():
         L = C.CDLL(LIB_PATH)
         vp, u64, u32, i32 = C.c_void_p, C.c_uint64, C.c_uint32, C.c_int
         tp = C.POINTER(_Table)
+        kcp, kbp = C.POINTER(_Kv4Cache), C.POINTER(_Kv4Batch)
         sig = {
             "lt_decode_lz4": (i32, [tp, vp, vp, vp]),
             "lt_dequant_int4": (i32, [vp, vp, vp, u64, u64, u64, vp, vp]),
@@ -134,6 +166,13 @@ def _lib():
             "lt_order_chunks_by_sequences": (i32, [vp, vp, u32, vp]),
             "lt_gemm_workspace_bytes": (u64, [u32, u32]),
             "lt_fused_lz4_int4_gemm": (i32, [tp, vp, vp, u64, u64, u64, vp, u32, vp, vp, u64, vp, vp]),
+            "lt_gemv_int4": (i32, [vp, vp, vp, u64, u64, u64, vp, u64, u32, i32, vp, u64, i32, vp]),
+            "lt_kv4_page_bytes": (u64, [u32, u32, u32]),
+            "lt_kv4_append": (i32, [kcp, kbp, C.POINTER(_Kv4New), vp, vp]),
+            "lt_kv4_read": (i32, [kcp, kbp, vp, vp, i32, vp, vp]),
+            "lt_kv4_attention_workspace_bytes": (u64, [kcp, kbp, u32, u32, u32]),
+            "lt_kv4_attention": (i32, [kcp, kbp, vp, C.c_int64, C.c_int64, u32, i32, C.c_float, u32, u32, vp,
+                                       C.c_int64, C.c_int64, vp, vp, u64, vp]),
             "lt_status_str": (C.c_char_p, [i32]),
             "lt_abi_version": (i32, []),
         }
@@ -586,6 +625,234 @@ def fused_lz4_int8(table: ChunkTable, scales, zp, shape, group: int, out=None, s
                                     _dptr(out), _dptr(status), _stream_ptr(stream)),
            "lt_fused_lz4_int8")
     return out.view(rows, cols)
+
+
+# ------------------------------------------------- operators on 4-bit memory
+
+def _dtype(t, fp32=False):
+    """The lt_dtype of a torch type (LT_F32 only where `fp32` is true)."""
+    torch = _torch()
+    if t == torch.float16:
+        return F16
+    if t == torch.bfloat16:
+        return BF16
+    if fp32 and t == torch.float32:
+        return F32
+    raise TypeError("float16 or bfloat16%s wanted, not %s" % (", or float32," if fp32 else "", t))
+
+
+def _heads3(x, name, tokens, heads, dim):
+    """Token and head strides of a [tokens, heads, dim] tensor whose last dimension is contiguous."""
+    if tuple(x.shape) != (tokens, heads, dim):
+        raise ValueError("%s must be [%d, %d, %d]" % (name, tokens, heads, dim))
+    if x.stride(2) != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    return x.stride(0), x.stride(1)
+
+
+def _i32(x, name, *shape):
+    torch = _torch()
+    if x.dtype != torch.int32 or not x.is_contiguous() or tuple(x.shape) != shape:
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, shape))
+
+
+def gemv_int4(packed, scales, zp, shape, group: int, x, y=None, dtype=None, stream=None):
+    """y = x W^T for 1 to 64 vectors, W the rows x cols matrix of packed INT4
+    codes (dequant_int4's arguments), never expanded and not rounded on the
+    way: x fp16 or bf16 [batch, cols] (or [cols]), rows any stride apart;
+    returns y [batch, rows] (or [rows]) of `dtype` (fp16, bf16 or fp32;
+    default x's)."""
+    torch = _torch()
+    rows, cols = _shape(shape)
+    flat = x.dim() == 1
+    if x.dim() not in (1, 2) or int(x.shape[-1]) != cols or x.stride(-1) != 1:
+        raise ValueError("x must be [batch, %d], contiguous in its last dimension" % cols)
+    batch = 1 if flat else int(x.shape[0])
+    if y is None:
+        y = torch.empty((rows,) if flat else (batch, rows), dtype=dtype or x.dtype, device=x.device)
+    elif tuple(y.shape) != ((rows,) if flat else (batch, rows)) or y.stride(-1) != 1 or dtype not in (None, y.dtype):
+        raise ValueError("y must be [batch, %d] of the wanted type, contiguous in its last dimension" % rows)
+    # a single row's stride is never used, but must hold a row
+    xs, ys = (cols, rows) if batch == 1 else (x.stride(0), y.stride(0))
+    _check(_lib().lt_gemv_int4(_dptr(packed), _dptr(scales), _dptr(zp), rows, cols, group, _dptr(x), xs, batch,
+                               _dtype(x.dtype), _dptr(y), ys, _dtype(y.dtype, True), _stream_ptr(stream)),
+           "lt_gemv_int4")
+    return y
+
+
+def kv4_page_bytes(page_tokens: int, head_dim: int, group: int) -> int:
+    """Bytes of one page and kv head of a 4-bit cache."""
+    n = int(_lib().lt_kv4_page_bytes(page_tokens, head_dim, group))
+    if n == 0:
+        raise LtError(LT_ERR_UNSUPPORTED, "lt_kv4_page_bytes")
+    return n
+
+
+@dataclass
+class Kv4Cache:
+    """A paged key/value cache in 4 bits (lt_kv4_cache in include/lt.h has the layout)."""
+    pages: object           # torch.uint8 [n_pages, kv_heads, kv4_page_bytes(...)], contiguous
+    page_tokens: int
+    kv_heads: int
+    head_dim: int
+    group: int
+
+    @classmethod
+    def empty(cls, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, group: int = 64, device="cuda"):
+        """A cache of n_pages pages; what they hold before kv4_append is never used."""
+        b = kv4_page_bytes(page_tokens, head_dim, group)
+        return cls(_torch().empty((n_pages, kv_heads, b), dtype=_torch().uint8, device=device), page_tokens, kv_heads,
+                   head_dim, group)
+
+    def as_c(self) -> _Kv4Cache:
+        p = self.pages
+        b = int(_lib().lt_kv4_page_bytes(self.page_tokens, self.head_dim, self.group))
+        if b and (p.dim() != 3 or p.shape[1] != self.kv_heads or p.shape[2] != b or p.element_size() != 1 or
+                  not p.is_contiguous()):
+            raise ValueError("pages must be a contiguous uint8 tensor [n_pages, %d, %d]" % (self.kv_heads, b))
+        return _Kv4Cache(p.data_ptr(), p.shape[0], self.page_tokens, self.kv_heads, self.head_dim, self.group)
+
+
+@dataclass
+class Kv4Batch:
+    """The rows of one step over a Kv4Cache (lt_kv4_batch in include/lt.h):
+    rows q_start[i] .. q_start[i+1] - 1 are the newest tokens of sequence i,
+    whose cache holds kv_len[i] tokens with them in the pages page_table[i]."""
+    q_start: object         # torch.int32 [n_seqs + 1]
+    kv_len: object          # torch.int32 [n_seqs]
+    page_table: object      # torch.int32 [n_seqs, max_pages]
+    n_tokens: int
+    max_q_len: int
+    max_kv_len: int
+
+    def as_c(self) -> _Kv4Batch:
+        n, width = self.page_table.shape
+        _i32(self.page_table, "page_table", n, width)
+        _i32(self.kv_len, "kv_len", n)
+        _i32(self.q_start, "q_start", n + 1)
+        return _Kv4Batch(self.q_start.data_ptr(), self.kv_len.data_ptr(), self.page_table.data_ptr(), n, width,
+                         self.n_tokens, self.max_q_len, self.max_kv_len)
+
+
+def kv4_append(cache: Kv4Cache, batch: Kv4Batch, k, v, q=None, q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+               cos=None, sin=None, neighbours: bool = False, positions=None, status=None, stream=None):
+    """Write the step's keys and values (fp16 or bf16 [n_tokens, kv_heads,
+    head_dim], any token and head strides) into the cache.  k and the queries
+    q [n_tokens, heads, head_dim] beside it first get their head norm (weights
+    q_norm, k_norm [head_dim], or None) and the rotation of their positions
+    (cos, sin fp32 [rope_len, rotary_dim / 2], pairs half a rotary_dim apart,
+    or neighbouring); all in one launch.  Returns q after both, in q_out
+    (allocated here when None), or None without q.  status (int32
+    [n_tokens]) receives CHUNK_OK or CHUNK_BAD_TABLE per token."""
+    torch = _torch()
+    T, dim = batch.n_tokens, cache.head_dim
+    ks, vs = _heads3(k, "k", T, cache.kv_heads, dim), _heads3(v, "v", T, cache.kv_heads, dim)
+    kind, heads, qs, os_ = _dtype(k.dtype), 0, (0, 0), (0, 0)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [n_tokens, heads, head_dim]")
+        heads = int(q.shape[1])
+        qs = _heads3(q, "q", T, heads, dim)
+        if q_out is None:
+            q_out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+        os_ = _heads3(q_out, "q_out", T, heads, dim)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    for x, name in ((v, "v"), (q, "q"), (q_out, "q_out"), (q_norm, "q_norm"), (k_norm, "k_norm")):
+        if x is not None and x.dtype != k.dtype:
+            raise TypeError("%s must have the type of k" % name)
+    for x, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if x is not None and (tuple(x.shape) != (dim,) or not x.is_contiguous()):
+            raise ValueError("%s must be a contiguous tensor of head_dim values" % name)
+    rope_len = rotary = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32 or \
+                not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous float32 tensors [rope_len, rotary_dim / 2]")
+        rope_len, rotary = int(cos.shape[0]), 2 * int(cos.shape[1])
+    if positions is not None:
+        _i32(positions, "positions", T)
+    if status is not None:
+        _i32(status, "status", T)
+    n = _Kv4New(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
+                None if q is None else q_out.data_ptr(), *ks, *vs, *qs, *os_,
+                None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
+                None if positions is None else positions.data_ptr(), heads, rope_len, rotary, int(neighbours), eps, kind)
+    c, b = cache.as_c(), batch.as_c()
+    if T > 0:
+        _check(_lib().lt_kv4_append(C.byref(c), C.byref(b), C.byref(n), _dptr(status), _stream_ptr(stream)),
+               "lt_kv4_append")
+    return q_out
+
+
+def kv4_read(cache: Kv4Cache, batch: Kv4Batch, dtype=None, k=None, v=None, status=None, stream=None):
+    """The keys and values that the cache stands for at the step's rows:
+    (k, v) of `dtype` (fp16, bf16 or fp32; default fp16) [n_tokens, kv_heads,
+    head_dim].  A batch whose q_start counts whole sequences reads them whole."""
+    torch = _torch()
+    shape = (batch.n_tokens, cache.kv_heads, cache.head_dim)
+    dev = cache.pages.device
+    if k is None:
+        k = torch.empty(shape, dtype=dtype or torch.float16, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype or k.dtype, device=dev)
+    for x in (k, v):
+        if tuple(x.shape) != shape or not x.is_contiguous() or x.dtype != (dtype or k.dtype):
+            raise ValueError("k and v must be contiguous [n_tokens, kv_heads, head_dim] tensors of one type")
+    if status is not None:
+        _i32(status, "status", batch.n_tokens)
+    c, b = cache.as_c(), batch.as_c()
+    if batch.n_tokens > 0:
+        _check(_lib().lt_kv4_read(C.byref(c), C.byref(b), _dptr(k), _dptr(v), _dtype(k.dtype, True), _dptr(status),
+                                  _stream_ptr(stream)), "lt_kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(cache: Kv4Cache, batch: Kv4Batch, heads: int, window: int = 0, sinks: int = 0) -> int:
+    c, b = cache.as_c(), batch.as_c()
+    return int(_lib().lt_kv4_attention_workspace_bytes(C.byref(c), C.byref(b), heads, window, sinks))
+
+
+def kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, scale: float = None, window: int = 0, sinks: int = 0, out=None,
+                  lse=None, workspace=None, stream=None):
+    """Causal attention of the step's queries q (fp16 or bf16 [n_tokens,
+    heads, head_dim], any token and head strides) over the cache.  With a
+    window, a row at position p sees the positions after p - window and the
+    first `sinks` ones.  scale defaults to head_dim ** -0.5.  Returns out
+    [n_tokens, heads, head_dim]; lse (fp32 [n_tokens, heads]) receives the
+    log-sum-exp of the scores.  The joins of split caches go through
+    `workspace` (uint8, kv4_attention_workspace_bytes; allocated here when
+    None)."""
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tokens, heads, head_dim]")
+    T, heads, dim = batch.n_tokens, int(q.shape[1]), cache.head_dim
+    qs = _heads3(q, "q", T, heads, dim)
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype:
+        raise TypeError("out must have the type of q")
+    os_ = _heads3(out, "out", T, heads, dim)
+    if lse is not None and (tuple(lse.shape) != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [n_tokens, heads]")
+    kind = _dtype(q.dtype)
+    c, b = cache.as_c(), batch.as_c()
+    if T == 0:
+        return out
+    need = int(_lib().lt_kv4_attention_workspace_bytes(C.byref(c), C.byref(b), heads, window, sinks))
+    own = workspace is None and need > 0
+    if own:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(_lib().lt_kv4_attention(C.byref(c), C.byref(b), _dptr(q), *qs, heads, kind,
+                                   dim ** -0.5 if scale is None else scale, window, sinks, _dptr(out), *os_, _dptr(lse),
+                                   _dptr(workspace), 0 if workspace is None else workspace.numel(),
+                                   _stream_ptr(stream)), "lt_kv4_attention")
+    if own and stream is not None:   # dropped on return while the launch still uses it
+        workspace.record_stream(stream)
+    return out
 
 
 # -------------------------------------------------------------- zero runs

@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +27,7 @@ HIP_FLAGS = [
 
 
 DEBUG_LIB = os.path.join(PKG, "liblt_debug.so")
+OPERATORS = ("lt_mv4", "lt_kv4")   # one source each, without debug checks of their own
 
 
 def build(verbose: bool = False, debug: bool = True) -> str:
@@ -36,20 +38,19 @@ def build(verbose: bool = False, debug: bool = True) -> str:
     pack_o = os.path.join(BUILD, "lt_pack.o")
     api_o = os.path.join(BUILD, "lt_api.o")
     dbg_o = os.path.join(BUILD, "lt_api_debug.o")
-    cmds = [
+    ops = [(os.path.join(CSRC, n + ".hip"), os.path.join(BUILD, n + ".o")) for n in OPERATORS]
+    objs = [o for _, o in ops] + [pack_o, "-pthread"]
+    compile_ = [
         ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-pthread", "-I" + os.path.join(ROOT, "include"), "-c",
          os.path.join(CSRC, "lt_pack.cpp"), "-o", pack_o],
         [HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, "lt_api.hip"), "-o", api_o],
-        [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", api_o, pack_o, "-pthread",
-         "-o", LIB + ".tmp"],
-    ]
+    ] + [[HIPCC, *HIP_FLAGS, "-c", src, "-o", o] for src, o in ops]
+    link = [[HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", api_o, *objs, "-o", LIB + ".tmp"]]
     if debug:
-        cmds += [
-            [HIPCC, *HIP_FLAGS, "-DLT_DEBUG", "-c", os.path.join(CSRC, "lt_api.hip"), "-o", dbg_o],
-            [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", dbg_o, pack_o, "-pthread",
-             "-o", DEBUG_LIB + ".tmp"],
-        ]
-    for c in cmds:
+        compile_.append([HIPCC, *HIP_FLAGS, "-DLT_DEBUG", "-c", os.path.join(CSRC, "lt_api.hip"), "-o", dbg_o])
+        link.append([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", dbg_o, *objs, "-o", DEBUG_LIB + ".tmp"])
+
+    def step(c):
         if verbose:
             print(" ".join(c), flush=True)
         r = subprocess.run(c, capture_output=True, text=True)
@@ -59,6 +60,11 @@ def build(verbose: bool = False, debug: bool = True) -> str:
             raise RuntimeError("build step failed: %s\n%s" % (" ".join(c), err))
         if verbose and err.strip():
             print(err, file=sys.stderr)
+
+    with ThreadPoolExecutor(max_workers=len(compile_)) as pool:   # the sources compile side by side
+        list(pool.map(step, compile_))
+    for c in link:
+        step(c)
     os.replace(LIB + ".tmp", LIB)
     if debug:
         os.replace(DEBUG_LIB + ".tmp", DEBUG_LIB)

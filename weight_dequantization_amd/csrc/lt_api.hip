@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "lt.h"
+#include "lt_args.hpp"
 #include "lt_device.hpp"
 #include "lt_lz4.hpp"
 #include "lt_verify.hpp"
@@ -245,22 +246,9 @@ __global__ void __launch_bounds__(RAW_THREADS) dequant_int8_kernel(RawParams P) 
 
 namespace {
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
-
-// rows*cols elements in groups of `group`; see lt.h for the rule.
-bool shape_ok(uint64_t rows, uint64_t cols, uint64_t group) {
-  if (rows == 0 || cols == 0 || group == 0) return false;
-  if (rows > (~0ull) / cols) return false;
-  uint64_t n = rows * cols;
-  if (n > (1ull << 48)) return false;
-  if (cols % group != 0 && group % cols != 0) return false;
-  if (n % group != 0) return false;
-  return true;
-}
-
-uint32_t shift_of(uint64_t g) {
-  return (g & (g - 1)) == 0 ? (uint32_t)__builtin_ctzll(g) : 64u;
-}
+using lt::aligned16;
+using lt::shape_ok;
+using lt::shift_of;
 
 template <int MODE, bool SPEC, bool LPF = false>
 void launch_kernel(bool small, hipStream_t s, const lt::ChunkParams &P) {

@@ -1,0 +1,199 @@
+// lt_kv4.hip -- liblt's entry points for the 4-bit key/value cache: argument
+// checks and launches.  Nothing here allocates, synchronizes or keeps state.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lt.h"
+#include "lt_args.hpp"
+#include "lt_kv4.hpp"
+
+namespace {
+
+using lt::aligned16;
+
+bool served(uint32_t page_tokens, uint32_t dim, uint32_t group) {
+  if (page_tokens != 32 && page_tokens != 64 && page_tokens != 128 && page_tokens != 256) return false;
+  if (dim != 64 && dim != 128 && dim != 256) return false;
+  return (group == 32 || group == 64 || group == 128 || group == 256) && group <= dim;
+}
+
+// The views the kernels take, or why the structs cannot be served.
+lt_status views(const lt_kv4_cache *c, const lt_kv4_batch *b, lt::Kv4View &C, lt::Kv4Rows &B) {
+  if (!c || !b) return LT_ERR_INVALID_ARG;
+  if (!c->pages || !aligned16(c->pages) || c->n_pages == 0 || c->kv_heads == 0) return LT_ERR_INVALID_ARG;
+  if (b->n_seqs > 0 && (!b->q_start || !b->kv_len || !b->page_table || b->max_pages == 0)) return LT_ERR_INVALID_ARG;
+  if ((((uintptr_t)b->q_start | (uintptr_t)b->kv_len | (uintptr_t)b->page_table) & 3) != 0) return LT_ERR_INVALID_ARG;
+  if (!served(c->page_tokens, c->head_dim, c->group)) return LT_ERR_UNSUPPORTED;
+  if (c->n_pages > 0x7FFFFFFFull || c->kv_heads > 65535 || b->n_tokens > 0x7FFFFFFFu || b->n_seqs > 0x7FFFFFFFu)
+    return LT_ERR_UNSUPPORTED;
+  C.pages = c->pages;
+  C.n_pages = c->n_pages;
+  C.kv_heads = c->kv_heads;
+  C.page_shift = lt::shift_of(c->page_tokens);
+  C.dim = c->head_dim;
+  C.group = c->group;
+  C.kc = c->page_tokens * c->head_dim / 2;
+  C.sc = c->page_tokens * (c->head_dim / c->group) * 4;
+  C.block = 2 * (C.kc + C.sc);
+  B.q_start = b->q_start;
+  B.kv_len = b->kv_len;
+  B.table = b->page_table;
+  B.n_seqs = b->n_seqs;
+  B.max_pages = b->max_pages;
+  B.n_tokens = b->n_tokens;
+  return LT_OK;
+}
+
+bool rows_ok(const void *p, int64_t ts, int64_t hs) { return p && aligned16(p) && ts % 8 == 0 && hs % 8 == 0; }
+
+lt_status launched() { return hipGetLastError() == hipSuccess ? LT_OK : LT_ERR_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+uint64_t lt_kv4_page_bytes(uint32_t page_tokens, uint32_t head_dim, uint32_t group) {
+  if (!served(page_tokens, head_dim, group)) return 0;
+  return (uint64_t)page_tokens * head_dim + 8ull * page_tokens * (head_dim / group);
+}
+
+lt_status lt_kv4_append(const lt_kv4_cache *cache, const lt_kv4_batch *batch, const lt_kv4_new *rows,
+                        int32_t *token_status, void *stream) {
+  lt::Kv4View C;
+  lt::Kv4Rows B;
+  const lt_status st = views(cache, batch, C, B);
+  if (st != LT_OK) return st;
+  if (!rows || (rows->type != LT_F16 && rows->type != LT_BF16)) return LT_ERR_INVALID_ARG;
+  if (!rows_ok(rows->k, rows->k_token_stride, rows->k_head_stride) ||
+      !rows_ok(rows->v, rows->v_token_stride, rows->v_head_stride))
+    return LT_ERR_INVALID_ARG;
+  if ((rows->q != nullptr) != (rows->q_out != nullptr)) return LT_ERR_INVALID_ARG;
+  if (rows->q && (rows->heads == 0 || rows->heads > 65535 ||
+                  !rows_ok(rows->q, rows->q_token_stride, rows->q_head_stride) ||
+                  !rows_ok(rows->q_out, rows->q_out_token_stride, rows->q_out_head_stride)))
+    return LT_ERR_INVALID_ARG;
+  if (!aligned16(rows->q_norm) || !aligned16(rows->k_norm)) return LT_ERR_INVALID_ARG;
+  if ((rows->q_norm || rows->k_norm) && !(rows->eps >= 0.0f)) return LT_ERR_INVALID_ARG;
+  if ((rows->cos != nullptr) != (rows->sin != nullptr)) return LT_ERR_INVALID_ARG;
+  if (rows->cos && (!aligned16(rows->cos) || !aligned16(rows->sin) || rows->rotary_dim == 0 ||
+                    rows->rotary_dim % 16 != 0 || rows->rotary_dim > C.dim || rows->rope_len == 0))
+    return LT_ERR_INVALID_ARG;
+  if ((((uintptr_t)rows->positions | (uintptr_t)token_status) & 3) != 0) return LT_ERR_INVALID_ARG;
+  if (B.n_tokens == 0) return LT_OK;
+  lt::Kv4NewRows N;
+  N.k = (const uint16_t *)rows->k;
+  N.v = (const uint16_t *)rows->v;
+  N.q = (const uint16_t *)rows->q;
+  N.q_out = (uint16_t *)rows->q_out;
+  N.k_ts = rows->k_token_stride;
+  N.k_hs = rows->k_head_stride;
+  N.v_ts = rows->v_token_stride;
+  N.v_hs = rows->v_head_stride;
+  N.q_ts = rows->q_token_stride;
+  N.q_hs = rows->q_head_stride;
+  N.o_ts = rows->q_out_token_stride;
+  N.o_hs = rows->q_out_head_stride;
+  N.q_norm = (const uint16_t *)rows->q_norm;
+  N.k_norm = (const uint16_t *)rows->k_norm;
+  N.cos = rows->cos;
+  N.sin = rows->sin;
+  N.positions = rows->positions;
+  N.status = token_status;
+  N.heads = rows->q ? rows->heads : 0;
+  N.rope_len = rows->rope_len;
+  N.rotary = rows->cos ? rows->rotary_dim : 0;
+  N.neighbours = rows->neighbours != 0;
+  N.bf16 = rows->type == LT_BF16;
+  N.eps = rows->eps;
+  const uint32_t per = 512 / C.dim;   // tokens a wave takes
+  const uint64_t waves = (uint64_t)((B.n_tokens + per - 1) / per) * (N.heads + 2ull * C.kv_heads);
+  if ((waves + 3) / 4 > 0x7FFFFFFFull) return LT_ERR_UNSUPPORTED;
+  const dim3 grid((uint32_t)((waves + 3) / 4));
+  hipStream_t s = (hipStream_t)stream;
+  switch (C.dim) {
+    case 64: hipLaunchKernelGGL(lt::kv4_append_kernel<8>, grid, dim3(256), 0, s, C, B, N); break;
+    case 128: hipLaunchKernelGGL(lt::kv4_append_kernel<16>, grid, dim3(256), 0, s, C, B, N); break;
+    default: hipLaunchKernelGGL(lt::kv4_append_kernel<32>, grid, dim3(256), 0, s, C, B, N); break;
+  }
+  return launched();
+}
+
+lt_status lt_kv4_read(const lt_kv4_cache *cache, const lt_kv4_batch *batch, void *k, void *v, lt_dtype type,
+                      int32_t *token_status, void *stream) {
+  lt::Kv4View C;
+  lt::Kv4Rows B;
+  const lt_status st = views(cache, batch, C, B);
+  if (st != LT_OK) return st;
+  if (type != LT_F16 && type != LT_BF16 && type != LT_F32) return LT_ERR_INVALID_ARG;
+  if ((!k && !v) || !aligned16(k) || !aligned16(v) || ((uintptr_t)token_status & 3) != 0) return LT_ERR_INVALID_ARG;
+  if (B.n_tokens == 0) return LT_OK;
+  const lt::Kv4ReadRows R{k, v, token_status, (uint32_t)type};
+  const uint32_t per = 512 / C.dim;
+  const uint64_t waves = (uint64_t)((B.n_tokens + per - 1) / per) * 2 * C.kv_heads;
+  if ((waves + 3) / 4 > 0x7FFFFFFFull) return LT_ERR_UNSUPPORTED;
+  const dim3 grid((uint32_t)((waves + 3) / 4));
+  hipStream_t s = (hipStream_t)stream;
+  switch (C.dim) {
+    case 64: hipLaunchKernelGGL(lt::kv4_read_kernel<8>, grid, dim3(256), 0, s, C, B, R); break;
+    case 128: hipLaunchKernelGGL(lt::kv4_read_kernel<16>, grid, dim3(256), 0, s, C, B, R); break;
+    default: hipLaunchKernelGGL(lt::kv4_read_kernel<32>, grid, dim3(256), 0, s, C, B, R); break;
+  }
+  return launched();
+}
+
+uint64_t lt_kv4_attention_workspace_bytes(const lt_kv4_cache *cache, const lt_kv4_batch *batch, uint32_t heads,
+                                          uint32_t window, uint32_t sinks) {
+  (void)cache;
+  (void)batch;
+  (void)heads;
+  (void)window;
+  (void)sinks;
+  return 0;
+}
+
+lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch, const void *q,
+                           int64_t q_token_stride, int64_t q_head_stride, uint32_t heads, lt_dtype type,
+                           float scale, uint32_t window, uint32_t sinks, void *out, int64_t out_token_stride,
+                           int64_t out_head_stride, float *lse, void *workspace, uint64_t workspace_bytes,
+                           void *stream) {
+  lt::Kv4View C;
+  lt::Kv4Rows B;
+  const lt_status st = views(cache, batch, C, B);
+  if (st != LT_OK) return st;
+  if (type != LT_F16 && type != LT_BF16) return LT_ERR_INVALID_ARG;
+  if (!rows_ok(q, q_token_stride, q_head_stride) || !rows_ok(out, out_token_stride, out_head_stride))
+    return LT_ERR_INVALID_ARG;
+  if (heads == 0 || heads % C.kv_heads != 0 || ((uintptr_t)lse & 3) != 0) return LT_ERR_INVALID_ARG;
+  if (!(scale > -3.4e38f && scale < 3.4e38f)) return LT_ERR_INVALID_ARG;
+  const uint64_t need = lt_kv4_attention_workspace_bytes(cache, batch, heads, window, sinks);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return LT_ERR_INVALID_ARG;
+  if (heads > 65535) return LT_ERR_UNSUPPORTED;
+  if (B.n_tokens == 0 || B.n_seqs == 0 || batch->max_q_len == 0) return LT_OK;
+  lt::Kv4Attn A;
+  A.q = (const uint16_t *)q;
+  A.out = (uint16_t *)out;
+  A.lse = lse;
+  A.q_ts = q_token_stride;
+  A.q_hs = q_head_stride;
+  A.o_ts = out_token_stride;
+  A.o_hs = out_head_stride;
+  A.heads = heads;
+  A.ratio = heads / C.kv_heads;
+  A.bf16 = type == LT_BF16;
+  A.window = window;
+  A.sinks = sinks;
+  A.max_q = batch->max_q_len;
+  A.scale = scale;
+  const uint64_t waves = (uint64_t)B.n_tokens * heads;
+  if ((waves + 3) / 4 > 0x7FFFFFFFull) return LT_ERR_UNSUPPORTED;
+  const dim3 grid((uint32_t)((waves + 3) / 4));
+  hipStream_t s = (hipStream_t)stream;
+  switch (C.dim) {
+    case 64: hipLaunchKernelGGL(lt::kv4_attention_kernel<1>, grid, dim3(256), 0, s, C, B, A); break;
+    case 128: hipLaunchKernelGGL(lt::kv4_attention_kernel<2>, grid, dim3(256), 0, s, C, B, A); break;
+    default: hipLaunchKernelGGL(lt::kv4_attention_kernel<4>, grid, dim3(256), 0, s, C, B, A); break;
+  }
+  return launched();
+}
+
+}  // extern "C"

@@ -48,6 +48,61 @@ bool rows_ok(const void *p, int64_t ts, int64_t hs) { return p && aligned16(p) &
 
 lt_status launched() { return hipGetLastError() == hipSuccess ? LT_OK : LT_ERR_LAUNCH; }
 
+// How an attention call is split over workgroups, from sizes known on the
+// host alone (so that the workspace can be asked for ahead).
+struct Plan {
+  bool wide;                 // waves over rows, not over tiles
+  uint32_t nt, unit, row_blocks, chunk, splits;
+  uint64_t bytes;
+};
+
+Plan plan_of(const lt::Kv4View &C, const lt::Kv4Rows &B, uint64_t max_q, uint64_t max_kv, uint32_t ratio,
+             uint32_t window, uint32_t sinks) {
+  Plan p;
+  const uint64_t rows = max_q * ratio;
+  p.wide = rows > (C.dim == 256 ? 16 : 32);
+  p.nt = C.dim == 256 || rows <= 16 || (p.wide && rows <= 64) ? 1 : 2;
+  p.unit = 16 * p.nt;
+  p.row_blocks = (uint32_t)((rows + p.unit * (p.wide ? 4 : 1) - 1) / (p.unit * (p.wide ? 4 : 1)));
+  // the most tiles a row sees, and the workgroups without a split
+  uint64_t tiles = (max_kv + 31) / 32;
+  if (window) {
+    const uint64_t kept = ((uint64_t)window + max_q + 31) / 32 + 1 + ((uint64_t)sinks + 31) / 32;
+    tiles = kept < tiles ? kept : tiles;
+  }
+  if (tiles < 1) tiles = 1;
+  const uint64_t units = (uint64_t)B.n_seqs * C.kv_heads * p.row_blocks;
+  uint64_t chunk = tiles;
+  if (p.wide) {
+    if (units < 256) chunk = (units * tiles + 511) / 512 < 32 ? 32 : (units * tiles + 511) / 512;
+  } else if (tiles > 16) {
+    chunk = (units * tiles + 1023) / 1024;
+    chunk = chunk < 16 ? 16 : chunk > 64 ? 64 : chunk;
+  }
+  p.chunk = (uint32_t)((chunk + 3) / 4 * 4);
+  p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
+  p.bytes = p.splits > 1 ? (uint64_t)B.n_tokens * C.kv_heads * ratio * p.splits * (C.dim + 2) * 4 : 0;
+  return p;
+}
+
+template <int D, int G, int NT, bool WIDE>
+void launch_rows(dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Rows &B, const lt::Kv4Attn &A) {
+  hipLaunchKernelGGL((lt::kv4_attention_kernel<D, G, NT, WIDE>), grid, dim3(256), 0, s, C, B, A);
+}
+
+template <int D, int G>
+void launch_attention(const Plan &p, dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Rows &B,
+                      const lt::Kv4Attn &A) {
+  constexpr int NT = D == 256 ? 1 : 2;   // more than 16 rows of 256 values do not fit a wave's registers
+  if (p.wide) {
+    p.nt == 1 ? launch_rows<D, G, 1, true>(grid, s, C, B, A) : launch_rows<D, G, NT, true>(grid, s, C, B, A);
+  } else {
+    p.nt == 1 ? launch_rows<D, G, 1, false>(grid, s, C, B, A) : launch_rows<D, G, NT, false>(grid, s, C, B, A);
+  }
+  if (p.splits > 1)
+    hipLaunchKernelGGL((lt::kv4_join_kernel<D>), dim3(B.n_tokens * A.heads), dim3(256), 0, s, C, B, A, p.unit);
+}
+
 }  // namespace
 
 extern "C" {
@@ -143,12 +198,10 @@ lt_status lt_kv4_read(const lt_kv4_cache *cache, const lt_kv4_batch *batch, void
 
 uint64_t lt_kv4_attention_workspace_bytes(const lt_kv4_cache *cache, const lt_kv4_batch *batch, uint32_t heads,
                                           uint32_t window, uint32_t sinks) {
-  (void)cache;
-  (void)batch;
-  (void)heads;
-  (void)window;
-  (void)sinks;
-  return 0;
+  lt::Kv4View C;
+  lt::Kv4Rows B;
+  if (views(cache, batch, C, B) != LT_OK || heads == 0 || heads % C.kv_heads != 0) return 0;
+  return plan_of(C, B, batch->max_q_len, batch->max_kv_len, heads / C.kv_heads, window, sinks).bytes;
 }
 
 lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch, const void *q,
@@ -165,9 +218,12 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
     return LT_ERR_INVALID_ARG;
   if (heads == 0 || heads % C.kv_heads != 0 || ((uintptr_t)lse & 3) != 0) return LT_ERR_INVALID_ARG;
   if (!(scale > -3.4e38f && scale < 3.4e38f)) return LT_ERR_INVALID_ARG;
-  const uint64_t need = lt_kv4_attention_workspace_bytes(cache, batch, heads, window, sinks);
-  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return LT_ERR_INVALID_ARG;
-  if (heads > 65535) return LT_ERR_UNSUPPORTED;
+  const Plan p = plan_of(C, B, batch->max_q_len, batch->max_kv_len, heads / C.kv_heads, window, sinks);
+  if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return LT_ERR_INVALID_ARG;
+  const uint64_t blocks = (uint64_t)B.n_seqs * C.kv_heads * p.row_blocks * p.splits;
+  if (heads > 65535 || blocks > 0x7FFFFFFFull || (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
+      (uint64_t)batch->max_q_len * (heads / C.kv_heads) > 0x7FFFFFFFull)
+    return LT_ERR_UNSUPPORTED;
   if (B.n_tokens == 0 || B.n_seqs == 0 || batch->max_q_len == 0) return LT_OK;
   lt::Kv4Attn A;
   A.q = (const uint16_t *)q;
@@ -183,15 +239,24 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
   A.window = window;
   A.sinks = sinks;
   A.max_q = batch->max_q_len;
-  A.scale = scale;
-  const uint64_t waves = (uint64_t)B.n_tokens * heads;
-  if ((waves + 3) / 4 > 0x7FFFFFFFull) return LT_ERR_UNSUPPORTED;
-  const dim3 grid((uint32_t)((waves + 3) / 4));
+  A.row_blocks = p.row_blocks;
+  A.chunk = p.chunk;
+  A.splits = p.splits;
+  A.part_o = (float *)workspace;
+  A.part_ml = p.bytes ? (float *)workspace + (uint64_t)B.n_tokens * heads * p.splits * C.dim : nullptr;
+  A.scale_log2 = scale * 1.4426950408889634f;
+  const dim3 grid((uint32_t)blocks);
   hipStream_t s = (hipStream_t)stream;
-  switch (C.dim) {
-    case 64: hipLaunchKernelGGL(lt::kv4_attention_kernel<1>, grid, dim3(256), 0, s, C, B, A); break;
-    case 128: hipLaunchKernelGGL(lt::kv4_attention_kernel<2>, grid, dim3(256), 0, s, C, B, A); break;
-    default: hipLaunchKernelGGL(lt::kv4_attention_kernel<4>, grid, dim3(256), 0, s, C, B, A); break;
+  switch (C.dim * 1024 + C.group) {
+    case 64 * 1024 + 32: launch_attention<64, 32>(p, grid, s, C, B, A); break;
+    case 64 * 1024 + 64: launch_attention<64, 64>(p, grid, s, C, B, A); break;
+    case 128 * 1024 + 32: launch_attention<128, 32>(p, grid, s, C, B, A); break;
+    case 128 * 1024 + 64: launch_attention<128, 64>(p, grid, s, C, B, A); break;
+    case 128 * 1024 + 128: launch_attention<128, 128>(p, grid, s, C, B, A); break;
+    case 256 * 1024 + 32: launch_attention<256, 32>(p, grid, s, C, B, A); break;
+    case 256 * 1024 + 64: launch_attention<256, 64>(p, grid, s, C, B, A); break;
+    case 256 * 1024 + 128: launch_attention<256, 128>(p, grid, s, C, B, A); break;
+    default: launch_attention<256, 256>(p, grid, s, C, B, A); break;
   }
   return launched();
 }

@@ -8,6 +8,11 @@
 
 namespace lt {
 
+template <bool V>
+struct kv4_bool {
+  static constexpr bool value = V;
+};
+
 struct Kv4View {
   uint8_t *pages;
   uint64_t n_pages;
@@ -310,67 +315,483 @@ struct Kv4Attn {
   float *lse;
   int64_t q_ts, q_hs, o_ts, o_hs;
   uint32_t heads, ratio, bf16, window, sinks, max_q;
-  float scale;
+  uint32_t row_blocks;       // workgroups over the rows of a sequence and kv head
+  uint32_t chunk, splits;    // 32-token tiles a workgroup takes, workgroups over a row's tiles
+  float *part_o, *part_ml;   // [n_tokens * heads][splits][dim], [..][2]: sums, reference and weight
+  float scale_log2;          // scale * log2(e)
 };
 
-// One wave per row and head, lane l holding values l, l + 64, ..; one token
-// after another with the running maximum and sum of the softmax.
-template <int DPL>
+// The tiles of 32 tokens that rows at positions p0 .. p1 see: 0 .. head - 1
+// (first tokens kept beside a window), then from `from` on, `total` in all.
+struct Kv4Tiles {
+  uint32_t head, from, total;
+};
+__device__ __forceinline__ Kv4Tiles kv4_tiles(int32_t p0, int32_t p1, uint32_t window, uint32_t sinks) {
+  const uint32_t hi = p1 < 0 ? 0 : (uint32_t)p1 + 1, end = (hi + 31) / 32;
+  const uint32_t first = p0 < 0 ? 0 : (uint32_t)p0 + 1;
+  const uint32_t lo = window && first > window ? first - window : 0;
+  Kv4Tiles t{0, lo / 32, end};
+  if (lo > 0) {
+    const uint32_t keep = ((sinks < hi ? sinks : hi) + 31) / 32;
+    t.head = keep < t.from ? keep : t.from;
+    t.total = t.head + end - t.from;
+  }
+  return t;
+}
+__device__ __forceinline__ uint32_t kv4_used(uint32_t total, const Kv4Attn &A) {
+  const uint32_t n = (total + A.chunk - 1) / A.chunk;
+  return n < 1 ? 1 : n < A.splits ? n : A.splits;
+}
+
+typedef uint32_t kv4_u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t kv4_u2 __attribute__((ext_vector_type(2)));
+typedef _Float16 kv4_h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 kv4_h2 __attribute__((ext_vector_type(2)));
+typedef float kv4_f4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float kv4_lo(uint32_t v) { return f32_of_f16((uint16_t)v); }
+__device__ __forceinline__ float kv4_hi(uint32_t v) { return f32_of_f16((uint16_t)(v >> 16)); }
+__device__ __forceinline__ uint32_t kv4_pair(float a, float b) {
+  const kv4_h2 h = {(_Float16)a, (_Float16)b};
+  return __builtin_bit_cast(uint32_t, h);
+}
+template <int N>
+__device__ __forceinline__ void kv4_load(uint32_t (&d)[N], const uint8_t *p) {   // N dwords, 8 or more bytes aligned
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const kv4_u4 v = *(const kv4_u4 *)(p + 4 * i);
+#pragma unroll
+      for (int k = 0; k < 4; k++) d[i + k] = v[k];
+    }
+  } else {
+    const kv4_u2 v = *(const kv4_u2 *)p;
+    d[0] = v[0];
+    d[1] = v[1];
+  }
+}
+__device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over lanes n, n + 16, n + 32, n + 48
+  float o = __shfl_xor(v, 16);
+  v = max ? fmaxf(v, o) : v + o;
+  o = __shfl_xor(v, 32);
+  return max ? fmaxf(v, o) : v + o;
+}
+
+// Attention on the matrix cores, NT tiles of 16 rows a wave, 32 tokens a step.
+// Rows are the queries of one sequence and kv head: row r is token r / ratio,
+// head r % ratio.  Lane (n, g) = (lane % 16, lane / 16).
+//
+// Scores, S^T = K Q^T: operand A has token n's codes in dims 32 c + 8 g + 0..7
+// for product c, straight from one load; two bits of masking turn 8 codes to
+// fp16 operands, since a nibble c at bit 0 of a half is the denormal c 2^-24
+// and at bit 4 the denormal c 2^-20 (matrix products keep fp16 denormals, and
+// products of q and codes are exact in fp32).  The query operand has the dims
+// in the same order, those at bit 4 divided by 16, each row scaled by a power
+// of two to a largest value in [2^12, 2^13), so bf16 and fp16 queries lose
+// nothing that fp32 would keep.  A group's scale and offset then go onto its
+// partial sum: q . k = sum_g s_g (q . c)_g + m_g sum_g q.
+// The result has row n's scores of tokens 4 g + 0..3 in a lane, so a row's
+// softmax state is the lane's own, shared by 4 lanes only.
+//
+// Output, O^T = V^T P^T: the weights are operand B exactly where the scores
+// came out; operand A has dims 64 h + 16 k + n of the step's tokens from one
+// load, unpacked like K's.  The value scales go onto the weights: p' = p s,
+// rounded to fp16 here and only here; what rounding does to the mean code is
+// kept out by taking codes from 8 on: sum p v = sum p' (c - 8) + sum p (m + 8 s),
+// with sum p' of the rounded weights.
+//
+// Running softmax: weights are 2^(x - ref); ref moves only when a weight times
+// the largest value scale so far would pass 2^15, and is then set so that it
+// is 2^7 (fp16 keeps 11 bits down to 2^-14).
+//
+// WIDE: the 4 waves of a workgroup take different rows and every tile.
+// Otherwise they share rows, take every 4th tile and join their sums.
+template <int D, int G, int NT, bool WIDE>
 __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B, Kv4Attn A) {
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint64_t w = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const uint64_t t64 = w / A.heads;
-  const uint32_t t = t64 < B.n_tokens ? (uint32_t)t64 : B.n_tokens;
-  const uint32_t head = (uint32_t)(w % A.heads), h = head / A.ratio;
-  const Kv4Token k = kv4_token<64>(C, B, t, lane);
+  constexpr int NG = D / G, KC = D / 32, VH = D / 64;
+  constexpr int CPG = G / 32;                        // score products of a group
+  constexpr int VALS = NT * VH * 4;                  // output registers of 4
+  __shared__ kv4_f4 join_o[WIDE ? 1 : 3][WIDE ? 1 : VALS][64];
+  __shared__ float join_ml[WIDE ? 1 : 3][WIDE ? 1 : NT][2][16];
+  const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t pairs = B.n_seqs * C.kv_heads;
+  const uint32_t pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
+  // late rows see the most tokens: they start first
+  const uint32_t rb = A.row_blocks - 1 - rest % A.row_blocks, split = rest / A.row_blocks;
+  const uint32_t seq = pair / C.kv_heads, h = pair % C.kv_heads;
+  const int32_t q0 = B.q_start[seq], q1 = B.q_start[seq + 1];
+  const int32_t kvl = B.kv_len[seq] > 0 ? B.kv_len[seq] : 0;
+  if (q0 < 0 || q1 <= q0 || (uint32_t)q1 > B.n_tokens) return;
+  const int32_t p_base = kvl - (q1 - q0);            // position of the first row
+  const uint32_t nq = (uint32_t)(q1 - q0) < A.max_q ? (uint32_t)(q1 - q0) : A.max_q;
+  const uint32_t rows = nq * A.ratio;
+  const uint32_t row0 = WIDE ? (rb * 4 + wave) * (NT * 16) : rb * (NT * 16);
+  if (row0 >= rows) return;
+  const uint32_t row1 = row0 + NT * 16 < rows ? row0 + NT * 16 : rows;
+  const int32_t p_first = p_base + (int32_t)(row0 / A.ratio), p_last = p_base + (int32_t)((row1 - 1) / A.ratio);
+  const Kv4Tiles tiles = kv4_tiles(p_first, p_last, A.window, A.sinks);
+  const uint32_t used = kv4_used(tiles.total, A);
+  if (split >= used) return;
+  const uint32_t i1 = split + 1 == A.splits || (split + 1) * A.chunk > tiles.total ? tiles.total : (split + 1) * A.chunk;
+
+  // the rows' queries, limits and softmax state
+  kv4_h8 qf[NT][KC];
+  float qs[NT][NG], cf[NT], ref[NT], top[NT], l[NT], off[NT][NG], rs[NT][NG];
+  uint32_t lim[NT], low[NT];
+  kv4_f4 o[NT][VH][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    uint32_t r = row0 + nt * 16 + n;
+    r = r < rows ? r : rows - 1;
+    const uint32_t t = r / A.ratio, hd = h * A.ratio + (r - t * A.ratio);
+    const int32_t p = p_base + (int32_t)t;
+    lim[nt] = p < 0 ? 0 : (uint32_t)p + 1;
+    low[nt] = A.window && lim[nt] > A.window ? lim[nt] - A.window : 0;
+    const uint16_t *src = A.q + (int64_t)(q0 + (int32_t)t) * A.q_ts + (int64_t)hd * A.q_hs + 8 * g;
+    float v[KC][8], most = 0.0f;
+#pragma unroll
+    for (int c = 0; c < KC; c++) {
+      load8(src + 32 * c, A.bf16 != 0, v[c]);
+#pragma unroll
+      for (int i = 0; i < 8; i++) most = fmaxf(most, fabsf(v[c][i]));
+    }
+    most = kv4_over_groups(most, true);
+    const int e = most > 0.0f ? 12 - ((int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127) : 0;
+    cf[nt] = ldexpf(fabsf(A.scale_log2), 24 - e);
+    const float sign = A.scale_log2 < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < NG; k++) qs[nt][k] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < KC; c++) {
+      _Float16 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        w[i] = (_Float16)(ldexpf(v[c][i], e) * sign);
+        qs[nt][c / CPG] += (float)w[i];
+      }
+      const _Float16 d16 = (_Float16)0.0625f;
+      qf[nt][c] = kv4_h8{w[0], w[4], w[1] * d16, w[5] * d16, w[2], w[6], w[3] * d16, w[7] * d16};
+    }
+#pragma unroll
+    for (int k = 0; k < NG; k++) {
+      qs[nt][k] = kv4_over_groups(qs[nt][k], false) * 5.9604644775390625e-8f;   // 2^-24
+      off[nt][k] = rs[nt][k] = 0.0f;
+    }
+    ref[nt] = -1e30f;                                // below any score: the first one that a row sees sets it
+    l[nt] = 0.0f;
+    top[nt] = -__builtin_inff();
+#pragma unroll
+    for (int k = 0; k < VH; k++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) o[nt][k][i] = kv4_f4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const uint32_t all_lim = p_first < 0 ? 0 : (uint32_t)p_first + 1;      // what every row sees ends here
+  const uint32_t any_lim = p_last < 0 ? 0 : (uint32_t)p_last + 1;
+  const uint32_t all_low = A.window && any_lim > A.window ? any_lim - A.window : 0;
+  const uint32_t any_low = A.window && all_lim > A.window ? all_lim - A.window : 0;
+  uint32_t e5 = 0;                                   // exponent field of the largest value scale so far
+  const uint32_t mask = (1u << C.page_shift) - 1;
+
+  auto step = [&](uint32_t j0, auto masked) {
+    constexpr bool MASKED = decltype(masked)::value;
+    const uint32_t pi = j0 >> C.page_shift, slot = j0 & mask;
+    int32_t page = pi < B.max_pages ? B.table[(uint64_t)seq * B.max_pages + pi] : -1;
+    const bool bad = page < 0 || (uint64_t)page >= C.n_pages;
+    const uint8_t *blk = kv4_block(C, bad ? 0u : (uint32_t)page, h);
+    const uint8_t *vblk = blk + C.kc + C.sc;
+    uint32_t kd[2][KC], vd[2][2 * VH], ks[2][NG][4], vs[2][NG][4];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      kv4_load(kd[u], blk + (slot + 16 * u + n) * (D / 2) + g * (D / 8));
+#pragma unroll
+      for (int k = 0; k < NG; k++) kv4_load(ks[u][k], blk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
+    }
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      kv4_load(vd[u], vblk + (slot + 16 * u) * (D / 2) + lane * (D / 8));
+#pragma unroll
+      for (int k = 0; k < NG; k++) kv4_load(vs[u][k], vblk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
+    }
+    float x[NT][2][4];
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int k = 0; k < NG; k++) {
+        kv4_f4 acc[NT];
+#pragma unroll
+        for (int c = k * CPG; c < (k + 1) * CPG; c++) {
+          const uint32_t w = kd[u][c], w8 = w >> 8;
+          const kv4_u4 a = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+            acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(kv4_h8, a), qf[nt][c],
+                                                             c % CPG ? acc[nt] : kv4_f4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const float y = k ? fmaf(kv4_hi(ks[u][k][i]), qs[nt][k], x[nt][u][i]) : kv4_hi(ks[u][k][i]) * qs[nt][k];
+            x[nt][u][i] = fmaf(kv4_lo(ks[u][k][i]), acc[nt][i], y);
+          }
+      }
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) x[nt][i >> 2][i & 3] = __builtin_nanf("");
+#pragma unroll
+        for (int k = 0; k < NG; k++) vs[i >> 2][k][i & 3] = 0;
+      }
+    }
+    bool vis[NT][2][4], part[2][NG][4];
+    if (MASKED) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const uint32_t j = j0 + 16 * u + 4 * g + i;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) vis[nt][u][i] = j < lim[nt] && (j >= low[nt] || j < A.sinks);
+          const bool any = j < any_lim && (j >= any_low || j < A.sinks);
+          // what no row sees, and what is not finite, has no part in the largest scale
+#pragma unroll
+          for (int k = 0; k < NG; k++) part[u][k][i] = any && (vs[u][k][i] & 0x7C00u) != 0x7C00u;
+        }
+    }
+    // does a weight times a value scale pass 2^15?
+    uint32_t sm = 0;
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int k = 0; k < NG; k++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const uint32_t b = !MASKED || part[u][k][i] ? vs[u][k][i] & 0x7FFFu : 0;
+          sm = sm > b ? sm : b;
+        }
+    float m[NT];
+    bool over = (sm >> 10) > e5;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      m[nt] = -__builtin_inff();
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) m[nt] = fmaxf(m[nt], !MASKED || vis[nt][u][i] ? x[nt][u][i] : -__builtin_inff());
+      over |= fmaf(cf[nt], m[nt], -ref[nt]) > (float)(29 - (int)e5);
+    }
+    if (__any(over)) {
+      uint32_t s5 = sm >> 10;
+      uint32_t t = (uint32_t)__shfl_xor((int)s5, 16);
+      s5 = s5 > t ? s5 : t;
+      t = (uint32_t)__shfl_xor((int)s5, 32);
+      s5 = s5 > t ? s5 : t;
+      e5 = __builtin_amdgcn_readfirstlane(e5 > s5 ? e5 : s5);
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        const float mm = kv4_over_groups(m[nt], true);
+        if (mm > -__builtin_inff()) top[nt] = fmaxf(top[nt], cf[nt] * mm);
+        if (top[nt] > -__builtin_inff()) {
+          const float r = top[nt] + (float)((int)e5 - 14 - 7);
+          const float a = __builtin_amdgcn_exp2f(ref[nt] - r);
+          ref[nt] = r;
+          l[nt] *= a;
+#pragma unroll
+          for (int k = 0; k < NG; k++) {
+            off[nt][k] *= a;
+            rs[nt][k] *= a;
+          }
+#pragma unroll
+          for (int k = 0; k < VH; k++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[nt][k][i] *= a;
+        }
+      }
+    }
+    // weights, times their value scales
+    uint32_t pf[NT][NG][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(cf[nt], x[nt][u][i], -ref[nt]));
+          if (MASKED) p[i] = vis[nt][u][i] ? p[i] : 0.0f;
+          l[nt] += p[i];
+        }
+#pragma unroll
+        for (int k = 0; k < NG; k++) {
+          float ps[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const float s = kv4_lo(vs[u][k][i]), mid = fmaf(8.0f, s, kv4_hi(vs[u][k][i]));
+            // a row that does not see the token must not meet what it holds
+            ps[i] = !MASKED || vis[nt][u][i] ? p[i] * s : 0.0f;
+            if (!MASKED || vis[nt][u][i]) off[nt][k] = fmaf(p[i], mid, off[nt][k]);
+          }
+          pf[nt][k][2 * u] = kv4_pair(ps[0], ps[1]);
+          pf[nt][k][2 * u + 1] = kv4_pair(ps[2], ps[3]);
+          const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+          rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, pf[nt][k][2 * u]), one, rs[nt][k], false);
+          rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, pf[nt][k][2 * u + 1]), one, rs[nt][k], false);
+        }
+      }
+#pragma unroll
+    for (int hh = 0; hh < VH; hh++)
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu;
+        const kv4_u4 a = {(vd[0][2 * hh] >> sh) & m4, (vd[0][2 * hh + 1] >> sh) & m4, (vd[1][2 * hh] >> sh) & m4,
+                          (vd[1][2 * hh + 1] >> sh) & m4};
+        const int grp = (64 * hh + 16 * k) / G;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          const kv4_u4 pb = {pf[nt][grp][0], pf[nt][grp][1], pf[nt][grp][2], pf[nt][grp][3]};
+          o[nt][hh][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(kv4_h8, a), __builtin_bit_cast(kv4_h8, pb),
+                                                                o[nt][hh][k], 0, 0, 0);
+        }
+      }
+  };
+
+  for (uint32_t i = split * A.chunk + (WIDE ? 0 : wave); i < i1; i += WIDE ? 1 : 4) {
+    const uint32_t j0 = 32 * (i < tiles.head ? i : tiles.from + (i - tiles.head));
+    if (j0 + 32 <= all_lim && (j0 >= all_low || j0 + 32 <= A.sinks))
+      step(j0, kv4_bool<false>{});
+    else
+      step(j0, kv4_bool<true>{});
+  }
+
+  // row sums over the 4 lanes of a row; outputs without their offsets
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    l[nt] = kv4_over_groups(l[nt], false);
+#pragma unroll
+    for (int k = 0; k < NG; k++) off[nt][k] = kv4_over_groups(fmaf(-8.0f, rs[nt][k], off[nt][k]), false);
+#pragma unroll
+    for (int hh = 0; hh < VH; hh++)
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          o[nt][hh][k][i] = fmaf(o[nt][hh][k][i], k & 1 ? 1048576.0f : 16777216.0f, off[nt][(64 * hh + 16 * k) / G]);
+  }
+  if (!WIDE) {
+    if (wave > 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+        for (int k = 0; k < VH * 4; k++) join_o[wave - 1][nt * VH * 4 + k][lane] = o[nt][k >> 2][k & 3];
+        if (g == 0) {
+          join_ml[wave - 1][nt][0][n] = ref[nt];
+          join_ml[wave - 1][nt][1][n] = l[nt];
+        }
+      }
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int w = 0; w < 3; w++) {
+        const float r2 = join_ml[w][nt][0][n], l2 = join_ml[w][nt][1][n];
+        // a side without weight counts for nothing, whatever its reference (NaN weights count)
+        const float r = l[nt] == 0.0f ? r2 : l2 == 0.0f ? ref[nt] : fmaxf(ref[nt], r2);
+        const float a = l[nt] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ref[nt] - r);
+        const float b = l2 == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(r2 - r);
+        ref[nt] = r;
+        l[nt] = l[nt] * a + l2 * b;
+#pragma unroll
+        for (int k = 0; k < VH * 4; k++)
+          o[nt][k >> 2][k & 3] = o[nt][k >> 2][k & 3] * a + join_o[w][nt * VH * 4 + k][lane] * b;
+      }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    const uint32_t r = row0 + nt * 16 + n;
+    if (r >= rows) continue;
+    const uint32_t t = r / A.ratio, hd = h * A.ratio + (r - t * A.ratio);
+    const uint64_t tok = (uint64_t)(uint32_t)q0 + t, at = tok * A.heads + hd;
+    if (used > 1) {
+      float *po = A.part_o + (at * A.splits + split) * D;
+#pragma unroll
+      for (int k = 0; k < VH * 4; k++) *(kv4_f4 *)(po + 16 * k + 4 * g) = o[nt][k >> 2][k & 3];
+      if (g == 0) {
+        A.part_ml[(at * A.splits + split) * 2] = ref[nt];
+        A.part_ml[(at * A.splits + split) * 2 + 1] = l[nt];
+      }
+    } else {
+      const float inv = l[nt] == 0.0f ? 0.0f : 1.0f / l[nt];
+      uint16_t *dst = A.out + (int64_t)tok * A.o_ts + (int64_t)hd * A.o_hs + 4 * g;
+#pragma unroll
+      for (int k = 0; k < VH * 4; k++) {
+        const kv4_f4 v = o[nt][k >> 2][k & 3];
+        const bool bf = A.bf16 != 0;
+        const kv4_u2 w = {(uint32_t)bits_of_f32(v[0] * inv, bf) | (uint32_t)bits_of_f32(v[1] * inv, bf) << 16,
+                          (uint32_t)bits_of_f32(v[2] * inv, bf) | (uint32_t)bits_of_f32(v[3] * inv, bf) << 16};
+        *(kv4_u2 *)(dst + 16 * k) = w;
+      }
+      if (A.lse && g == 0)
+        A.lse[at] = l[nt] == 0.0f ? -__builtin_inff() : 0.6931471805599453f * (ref[nt] + __log2f(l[nt]));
+    }
+  }
+}
+
+// Joins the splits of a row: one workgroup a row, D / 4 threads a split.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_join_kernel(Kv4View C, Kv4Rows B, Kv4Attn A, uint32_t unit) {
+  constexpr uint32_t T = D / 4, S = 256 / T;
+  __shared__ kv4_f4 sum_o[S][T];
+  __shared__ float sum_ml[S][2];
+  const uint32_t t = blockIdx.x / A.heads, hd = blockIdx.x % A.heads;
+  const uint32_t d = threadIdx.x % T, s0 = threadIdx.x / T;
   uint32_t cnt = 0;
-  for (uint32_t b = lane; b < B.n_seqs; b += 64) cnt += (uint32_t)(B.q_start[b + 1] <= (int32_t)t);
-  for (int d = 1; d < 64; d <<= 1) cnt += __shfl_xor(cnt, d);
-  if (t >= B.n_tokens || cnt >= B.n_seqs) return;
-  if (t - (uint32_t)B.q_start[cnt] >= A.max_q) return;
-  const uint32_t n = k.seq >= 0 ? (uint32_t)k.pos + 1 : 0;
-  const uint32_t lo = A.window && n > A.window ? n - A.window : 0;
-  float q[DPL], o[DPL], top = -__builtin_inff(), sum = 0.0f;
+  for (uint32_t b = threadIdx.x & 63u; b < B.n_seqs; b += 64) cnt += (uint32_t)(B.q_start[b + 1] <= (int32_t)t);
 #pragma unroll
-  for (int i = 0; i < DPL; i++) {
-    q[i] = f32_of_bits(A.q[(int64_t)t * A.q_ts + (int64_t)head * A.q_hs + lane + 64 * i], A.bf16 != 0);
-    o[i] = 0.0f;
+  for (int k = 1; k < 64; k <<= 1) cnt += __shfl_xor(cnt, k);
+  if (cnt >= B.n_seqs) return;
+  const int32_t q0 = B.q_start[cnt], q1 = B.q_start[cnt + 1];
+  const int32_t kvl = B.kv_len[cnt] > 0 ? B.kv_len[cnt] : 0;
+  if (q0 < 0 || (int32_t)t < q0 || (uint32_t)q1 > B.n_tokens || t - (uint32_t)q0 >= A.max_q) return;
+  // the tiles of the rows that were taken together with this one
+  const uint32_t nq = (uint32_t)(q1 - q0) < A.max_q ? (uint32_t)(q1 - q0) : A.max_q, rows = nq * A.ratio;
+  const uint32_t row0 = ((t - (uint32_t)q0) * A.ratio + hd % A.ratio) / unit * unit;
+  const uint32_t row1 = row0 + unit < rows ? row0 + unit : rows;
+  const int32_t p_base = kvl - (q1 - q0);
+  const Kv4Tiles tiles = kv4_tiles(p_base + (int32_t)(row0 / A.ratio), p_base + (int32_t)((row1 - 1) / A.ratio), A.window,
+                                   A.sinks);
+  const uint32_t used = kv4_used(tiles.total, A);
+  if (used <= 1) return;
+  const uint64_t at = (uint64_t)t * A.heads + hd;
+  const float *ml = A.part_ml + at * A.splits * 2, *po = A.part_o + at * A.splits * D + 4 * d;
+  float ref = 0.0f, l = 0.0f;
+  kv4_f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](float r2, float l2, kv4_f4 o2) {
+    const float r = l == 0.0f ? r2 : l2 == 0.0f ? ref : fmaxf(ref, r2);
+    const float a = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ref - r);
+    const float b = l2 == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(r2 - r);
+    ref = r;
+    l = l * a + l2 * b;
+    o = o * a + o2 * b;
+  };
+  for (uint32_t s = s0; s < used; s += S) add(ml[2 * s], ml[2 * s + 1], *(const kv4_f4 *)(po + (uint64_t)s * D));
+  sum_o[s0][d] = o;
+  if (d == 0) {
+    sum_ml[s0][0] = ref;
+    sum_ml[s0][1] = l;
   }
-  for (uint32_t p = A.sinks > 0 || lo == 0 ? 0 : lo; p < n; p++) {
-    if (p >= A.sinks && p < lo) p = lo;
-    const uint32_t pi = p >> C.page_shift, slot = p & ((1u << C.page_shift) - 1);
-    const int32_t page = pi < B.max_pages ? B.table[(uint64_t)cnt * B.max_pages + pi] : -1;
-    if (page < 0 || (uint64_t)page >= C.n_pages) {
-      sum = __builtin_nanf("");
-      continue;
-    }
-    const uint8_t *blk = kv4_block(C, (uint32_t)page, h);
-    float x = 0.0f, v[DPL];
-#pragma unroll
-    for (int i = 0; i < DPL; i++) {
-      const uint32_t d = lane + 64 * i, g = d / C.group, j = d / 8;
-      const uint32_t kb = blk[kv4_k_row(C, slot) + 4 * ((j & 3) * (C.dim / 32) + (j >> 2)) + (d & 7) / 2];
-      const uint32_t vb = *(const uint16_t *)(blk + C.kc + C.sc + kv4_v_unit(C, slot, d & 15, d >> 6));
-      const uint32_t ks = *(const uint32_t *)(blk + C.kc + kv4_scale(C, slot, g));
-      const uint32_t vs = *(const uint32_t *)(blk + 2 * C.kc + C.sc + kv4_scale(C, slot, g));
-      const float kd = fmaf((float)((kb >> (4 * (d & 1))) & 15u), f32_of_f16((uint16_t)ks), f32_of_f16((uint16_t)(ks >> 16)));
-      v[i] = fmaf((float)((vb >> (4 * ((d >> 4) & 3))) & 15u), f32_of_f16((uint16_t)vs), f32_of_f16((uint16_t)(vs >> 16)));
-      x = fmaf(q[i], kd, x);
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-    x *= A.scale;
-    const float nt = fmaxf(top, x), a = nt > top ? __expf(top - nt) : 1.0f, e = __expf(x - nt);
-    top = nt;
-    sum = fmaf(sum, a, e);
-#pragma unroll
-    for (int i = 0; i < DPL; i++) o[i] = fmaf(o[i], a, e * v[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < DPL; i++)
-    A.out[(int64_t)t * A.o_ts + (int64_t)head * A.o_hs + lane + 64 * i] =
-        bits_of_f32(sum == 0.0f ? 0.0f : o[i] / sum, A.bf16 != 0);
-  if (A.lse && lane == 0) A.lse[(uint64_t)t * A.heads + head] = sum == 0.0f ? -__builtin_inff() : top + logf(sum);
+  __syncthreads();
+  if (s0 > 0) return;
+  for (uint32_t s = 1; s < S; s++) add(sum_ml[s][0], sum_ml[s][1], sum_o[s][d]);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const bool bf = A.bf16 != 0;
+  const kv4_u2 w = {(uint32_t)bits_of_f32(o[0] * inv, bf) | (uint32_t)bits_of_f32(o[1] * inv, bf) << 16,
+                    (uint32_t)bits_of_f32(o[2] * inv, bf) | (uint32_t)bits_of_f32(o[3] * inv, bf) << 16};
+  *(kv4_u2 *)(A.out + (int64_t)t * A.o_ts + (int64_t)hd * A.o_hs + 4 * d) = w;
+  if (A.lse && d == 0) A.lse[at] = l == 0.0f ? -__builtin_inff() : 0.6931471805599453f * (ref + __log2f(l));
 }
 
 }  // namespace lt

@@ -306,13 +306,15 @@ def _torch():
 
 
 def _stream_ptr(stream=None):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    # the current device's current stream, without a Stream object on the way (0.2 us against 2.8)
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _dptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _place(a: np.ndarray, device, pin: bool):
@@ -641,19 +643,20 @@ def _dtype(t, fp32=False):
     raise TypeError("float16 or bfloat16%s wanted, not %s" % (", or float32," if fp32 else "", t))
 
 
-def _heads3(x, name, tokens, heads, dim):
+def _heads3(x, name, shape):
     """Token and head strides of a [tokens, heads, dim] tensor whose last dimension is contiguous."""
-    if tuple(x.shape) != (tokens, heads, dim):
-        raise ValueError("%s must be [%d, %d, %d]" % (name, tokens, heads, dim))
-    if x.stride(2) != 1:
+    if x.shape != shape:
+        raise ValueError("%s must be [%d, %d, %d]" % (name, *shape))
+    ts, hs, one = x.stride()
+    if one != 1:
         raise ValueError("%s must be contiguous in its last dimension" % name)
-    return x.stride(0), x.stride(1)
+    return ts, hs
 
 
 def _i32(x, name, *shape):
-    torch = _torch()
-    if x.dtype != torch.int32 or not x.is_contiguous() or tuple(x.shape) != shape:
+    if x.dtype is not _torch().int32 or x.shape != shape or not x.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, shape))
+    return x.data_ptr()
 
 
 def gemv_int4(packed, scales, zp, shape, group: int, x, y=None, dtype=None, stream=None):
@@ -662,15 +665,14 @@ def gemv_int4(packed, scales, zp, shape, group: int, x, y=None, dtype=None, stre
     way: x fp16 or bf16 [batch, cols] (or [cols]), rows any stride apart;
     returns y [batch, rows] (or [rows]) of `dtype` (fp16, bf16 or fp32;
     default x's)."""
-    torch = _torch()
     rows, cols = _shape(shape)
     flat = x.dim() == 1
     if x.dim() not in (1, 2) or int(x.shape[-1]) != cols or x.stride(-1) != 1:
         raise ValueError("x must be [batch, %d], contiguous in its last dimension" % cols)
     batch = 1 if flat else int(x.shape[0])
     if y is None:
-        y = torch.empty((rows,) if flat else (batch, rows), dtype=dtype or x.dtype, device=x.device)
-    elif tuple(y.shape) != ((rows,) if flat else (batch, rows)) or y.stride(-1) != 1 or dtype not in (None, y.dtype):
+        y = x.new_empty((rows,) if flat else (batch, rows), dtype=dtype)
+    elif y.shape != ((rows,) if flat else (batch, rows)) or y.stride(-1) != 1 or dtype not in (None, y.dtype):
         raise ValueError("y must be [batch, %d] of the wanted type, contiguous in its last dimension" % rows)
     # a single row's stride is never used, but must hold a row
     xs, ys = (cols, rows) if batch == 1 else (x.stride(0), y.stride(0))
@@ -705,12 +707,13 @@ class Kv4Cache:
                    head_dim, group)
 
     def as_c(self) -> _Kv4Cache:
-        p = self.pages
-        b = int(_lib().lt_kv4_page_bytes(self.page_tokens, self.head_dim, self.group))
-        if b and (p.dim() != 3 or p.shape[1] != self.kv_heads or p.shape[2] != b or p.element_size() != 1 or
-                  not p.is_contiguous()):
-            raise ValueError("pages must be a contiguous uint8 tensor [n_pages, %d, %d]" % (self.kv_heads, b))
-        return _Kv4Cache(p.data_ptr(), p.shape[0], self.page_tokens, self.kv_heads, self.head_dim, self.group)
+        p, P, D, G = self.pages, self.page_tokens, self.head_dim, self.group
+        # sizes that are not served are left for the library to refuse
+        if G > 0 and (p.dim() != 3 or p.shape[1:] != (self.kv_heads, P * D + 8 * P * (D // G)) or
+                      p.element_size() != 1 or not p.is_contiguous()):
+            raise ValueError("pages must be a contiguous uint8 tensor [n_pages, %d, %d]" %
+                             (self.kv_heads, P * D + 8 * P * (D // G)))
+        return _Kv4Cache(p.data_ptr(), p.shape[0], P, self.kv_heads, D, G)
 
 
 @dataclass
@@ -727,11 +730,9 @@ class Kv4Batch:
 
     def as_c(self) -> _Kv4Batch:
         n, width = self.page_table.shape
-        _i32(self.page_table, "page_table", n, width)
-        _i32(self.kv_len, "kv_len", n)
-        _i32(self.q_start, "q_start", n + 1)
-        return _Kv4Batch(self.q_start.data_ptr(), self.kv_len.data_ptr(), self.page_table.data_ptr(), n, width,
-                         self.n_tokens, self.max_q_len, self.max_kv_len)
+        return _Kv4Batch(_i32(self.q_start, "q_start", n + 1), _i32(self.kv_len, "kv_len", n),
+                         _i32(self.page_table, "page_table", n, width), n, width, self.n_tokens, self.max_q_len,
+                         self.max_kv_len)
 
 
 def kv4_append(cache: Kv4Cache, batch: Kv4Batch, k, v, q=None, q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
@@ -744,47 +745,46 @@ def kv4_append(cache: Kv4Cache, batch: Kv4Batch, k, v, q=None, q_out=None, q_nor
     or neighbouring); all in one launch.  Returns q after both, in q_out
     (allocated here when None), or None without q.  status (int32
     [n_tokens]) receives CHUNK_OK or CHUNK_BAD_TABLE per token."""
-    torch = _torch()
     T, dim = batch.n_tokens, cache.head_dim
-    ks, vs = _heads3(k, "k", T, cache.kv_heads, dim), _heads3(v, "v", T, cache.kv_heads, dim)
-    kind, heads, qs, os_ = _dtype(k.dtype), 0, (0, 0), (0, 0)
+    shape = (T, cache.kv_heads, dim)
+    ks, vs = _heads3(k, "k", shape), _heads3(v, "v", shape)
+    dtype, heads, qs, os_ = k.dtype, 0, (0, 0), (0, 0)
+    kind = _dtype(dtype)
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [n_tokens, heads, head_dim]")
-        heads = int(q.shape[1])
-        qs = _heads3(q, "q", T, heads, dim)
+        heads = q.shape[1]
+        shape = (T, heads, dim)
+        qs = _heads3(q, "q", shape)
         if q_out is None:
-            q_out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
-        os_ = _heads3(q_out, "q_out", T, heads, dim)
+            q_out = q.new_empty(shape)
+        os_ = _heads3(q_out, "q_out", shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     for x, name in ((v, "v"), (q, "q"), (q_out, "q_out"), (q_norm, "q_norm"), (k_norm, "k_norm")):
-        if x is not None and x.dtype != k.dtype:
+        if x is not None and x.dtype is not dtype:
             raise TypeError("%s must have the type of k" % name)
     for x, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if x is not None and (tuple(x.shape) != (dim,) or not x.is_contiguous()):
+        if x is not None and (x.shape != (dim,) or not x.is_contiguous()):
             raise ValueError("%s must be a contiguous tensor of head_dim values" % name)
     rope_len = rotary = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32 or \
+        f32 = _torch().float32
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype is not f32 or sin.dtype is not f32 or \
                 not cos.is_contiguous() or not sin.is_contiguous():
             raise ValueError("cos and sin must be contiguous float32 tensors [rope_len, rotary_dim / 2]")
-        rope_len, rotary = int(cos.shape[0]), 2 * int(cos.shape[1])
+        rope_len, rotary = cos.shape[0], 2 * cos.shape[1]
     if positions is not None:
-        _i32(positions, "positions", T)
+        positions = _i32(positions, "positions", T)
     if status is not None:
-        _i32(status, "status", T)
-    n = _Kv4New(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
-                None if q is None else q_out.data_ptr(), *ks, *vs, *qs, *os_,
-                None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-                None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
-                None if positions is None else positions.data_ptr(), heads, rope_len, rotary, int(neighbours), eps, kind)
+        status = _i32(status, "status", T)
+    n = _Kv4New(k.data_ptr(), v.data_ptr(), _dptr(q), _dptr(q_out), *ks, *vs, *qs, *os_, _dptr(q_norm), _dptr(k_norm),
+                _dptr(cos), _dptr(sin), positions, heads, rope_len, rotary, neighbours, eps, kind)
     c, b = cache.as_c(), batch.as_c()
     if T > 0:
-        _check(_lib().lt_kv4_append(C.byref(c), C.byref(b), C.byref(n), _dptr(status), _stream_ptr(stream)),
-               "lt_kv4_append")
+        _check(_lib().lt_kv4_append(c, b, n, status, _stream_ptr(stream)), "lt_kv4_append")
     return q_out
 
 
@@ -792,28 +792,25 @@ def kv4_read(cache: Kv4Cache, batch: Kv4Batch, dtype=None, k=None, v=None, statu
     """The keys and values that the cache stands for at the step's rows:
     (k, v) of `dtype` (fp16, bf16 or fp32; default fp16) [n_tokens, kv_heads,
     head_dim].  A batch whose q_start counts whole sequences reads them whole."""
-    torch = _torch()
     shape = (batch.n_tokens, cache.kv_heads, cache.head_dim)
-    dev = cache.pages.device
     if k is None:
-        k = torch.empty(shape, dtype=dtype or torch.float16, device=dev)
+        k = cache.pages.new_empty(shape, dtype=dtype or _torch().float16)
     if v is None:
-        v = torch.empty(shape, dtype=dtype or k.dtype, device=dev)
+        v = cache.pages.new_empty(shape, dtype=dtype or k.dtype)
     for x in (k, v):
-        if tuple(x.shape) != shape or not x.is_contiguous() or x.dtype != (dtype or k.dtype):
+        if x.shape != shape or not x.is_contiguous() or x.dtype is not (dtype or k.dtype):
             raise ValueError("k and v must be contiguous [n_tokens, kv_heads, head_dim] tensors of one type")
     if status is not None:
-        _i32(status, "status", batch.n_tokens)
+        status = _i32(status, "status", batch.n_tokens)
+    kind = _dtype(k.dtype, True)
     c, b = cache.as_c(), batch.as_c()
     if batch.n_tokens > 0:
-        _check(_lib().lt_kv4_read(C.byref(c), C.byref(b), _dptr(k), _dptr(v), _dtype(k.dtype, True), _dptr(status),
-                                  _stream_ptr(stream)), "lt_kv4_read")
+        _check(_lib().lt_kv4_read(c, b, k.data_ptr(), v.data_ptr(), kind, status, _stream_ptr(stream)), "lt_kv4_read")
     return k, v
 
 
 def kv4_attention_workspace_bytes(cache: Kv4Cache, batch: Kv4Batch, heads: int, window: int = 0, sinks: int = 0) -> int:
-    c, b = cache.as_c(), batch.as_c()
-    return int(_lib().lt_kv4_attention_workspace_bytes(C.byref(c), C.byref(b), heads, window, sinks))
+    return _lib().lt_kv4_attention_workspace_bytes(cache.as_c(), batch.as_c(), heads, window, sinks)
 
 
 def kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, scale: float = None, window: int = 0, sinks: int = 0, out=None,
@@ -826,32 +823,33 @@ def kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, scale: float = None, wind
     log-sum-exp of the scores.  The joins of split caches go through
     `workspace` (uint8, kv4_attention_workspace_bytes; allocated here when
     None)."""
-    torch = _torch()
     if q.dim() != 3:
         raise ValueError("q must be [n_tokens, heads, head_dim]")
-    T, heads, dim = batch.n_tokens, int(q.shape[1]), cache.head_dim
-    qs = _heads3(q, "q", T, heads, dim)
-    if out is None:
-        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype:
-        raise TypeError("out must have the type of q")
-    os_ = _heads3(out, "out", T, heads, dim)
-    if lse is not None and (tuple(lse.shape) != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 tensor [n_tokens, heads]")
+    T, heads, dim = batch.n_tokens, q.shape[1], cache.head_dim
+    shape = (T, heads, dim)
+    q_ts, q_hs = _heads3(q, "q", shape)
     kind = _dtype(q.dtype)
+    if out is None:
+        out = q.new_empty(shape)
+    elif out.dtype is not q.dtype:
+        raise TypeError("out must have the type of q")
+    o_ts, o_hs = _heads3(out, "out", shape)
+    if lse is not None:
+        if lse.shape != (T, heads) or lse.dtype is not _torch().float32 or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 tensor [n_tokens, heads]")
+        lse = lse.data_ptr()
     c, b = cache.as_c(), batch.as_c()
     if T == 0:
         return out
-    need = int(_lib().lt_kv4_attention_workspace_bytes(C.byref(c), C.byref(b), heads, window, sinks))
-    own = workspace is None and need > 0
-    if own:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(_lib().lt_kv4_attention(C.byref(c), C.byref(b), _dptr(q), *qs, heads, kind,
-                                   dim ** -0.5 if scale is None else scale, window, sinks, _dptr(out), *os_, _dptr(lse),
-                                   _dptr(workspace), 0 if workspace is None else workspace.numel(),
-                                   _stream_ptr(stream)), "lt_kv4_attention")
-    if own and stream is not None:   # dropped on return while the launch still uses it
-        workspace.record_stream(stream)
+    L, own = _lib(), None
+    if workspace is None:
+        size = L.lt_kv4_attention_workspace_bytes(c, b, heads, window, sinks)
+        own = workspace = cache.pages.new_empty(size) if size else None
+    _check(L.lt_kv4_attention(c, b, q.data_ptr(), q_ts, q_hs, heads, kind, dim ** -0.5 if scale is None else scale, window,
+                              sinks, out.data_ptr(), o_ts, o_hs, lse, _dptr(workspace),
+                              0 if workspace is None else workspace.numel(), _stream_ptr(stream)), "lt_kv4_attention")
+    if own is not None and stream is not None:   # dropped on return while the launch still uses it
+        own.record_stream(stream)
     return out
 
 

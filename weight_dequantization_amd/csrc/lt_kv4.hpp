@@ -8,11 +8,6 @@
 
 namespace lt {
 
-template <bool V>
-struct kv4_bool {
-  static constexpr bool value = V;
-};
-
 struct Kv4View {
   uint8_t *pages;
   uint64_t n_pages;
@@ -493,27 +488,42 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
   uint32_t e5 = 0;                                   // exponent field of the largest value scale so far
   const uint32_t mask = (1u << C.page_shift) - 1;
 
-  auto step = [&](uint32_t j0, auto masked) {
-    constexpr bool MASKED = decltype(masked)::value;
-    const uint32_t pi = j0 >> C.page_shift, slot = j0 & mask;
-    int32_t page = pi < B.max_pages ? B.table[(uint64_t)seq * B.max_pages + pi] : -1;
-    const bool bad = page < 0 || (uint64_t)page >= C.n_pages;
-    const uint8_t *blk = kv4_block(C, bad ? 0u : (uint32_t)page, h);
-    const uint8_t *vblk = blk + C.kc + C.sc;
+  // the first token of the i-th tile, and its page (-1: none)
+  auto first_of = [&](uint32_t i) { return 32 * (i < tiles.head ? i : tiles.from + (i - tiles.head)); };
+  auto page_of = [&](uint32_t j0) {
+    const uint32_t pi = j0 >> C.page_shift;
+    const int32_t page = pi < B.max_pages ? B.table[(uint64_t)seq * B.max_pages + pi] : -1;
+    return page >= 0 && (uint64_t)page < C.n_pages ? page : -1;
+  };
+
+  struct Tile {
+    uint32_t j0;
+    bool bad;
     uint32_t kd[2][KC], vd[2][2 * VH], ks[2][NG][4], vs[2][NG][4];
+  };
+  auto load = [&](Tile &T, uint32_t j0, int32_t page) {
+    T.j0 = j0;
+    T.bad = page < 0;
+    const uint32_t slot = j0 & mask;
+    const uint8_t *blk = kv4_block(C, T.bad ? 0u : (uint32_t)page, h);
+    const uint8_t *vblk = blk + C.kc + C.sc;
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      kv4_load(kd[u], blk + (slot + 16 * u + n) * (D / 2) + g * (D / 8));
+      kv4_load(T.kd[u], blk + (slot + 16 * u + n) * (D / 2) + g * (D / 8));
 #pragma unroll
-      for (int k = 0; k < NG; k++) kv4_load(ks[u][k], blk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
+      for (int k = 0; k < NG; k++) kv4_load(T.ks[u][k], blk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
     }
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      kv4_load(vd[u], vblk + (slot + 16 * u) * (D / 2) + lane * (D / 8));
+      kv4_load(T.vd[u], vblk + (slot + 16 * u) * (D / 2) + lane * (D / 8));
 #pragma unroll
-      for (int k = 0; k < NG; k++) kv4_load(vs[u][k], vblk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
+      for (int k = 0; k < NG; k++) kv4_load(T.vs[u][k], vblk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
     }
-    float x[NT][2][4];
+  };
+
+  auto step = [&](Tile &T) {
+    const uint32_t j0 = T.j0;
+    float x[NT][8];
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
         kv4_f4 acc[NT];
 #pragma unroll
         for (int c = k * CPG; c < (k + 1) * CPG; c++) {
-          const uint32_t w = kd[u][c], w8 = w >> 8;
+          const uint32_t w = T.kd[u][c], w8 = w >> 8;
           const kv4_u4 a = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
 #pragma unroll
           for (int nt = 0; nt < NT; nt++)
@@ -532,54 +542,57 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const float y = k ? fmaf(kv4_hi(ks[u][k][i]), qs[nt][k], x[nt][u][i]) : kv4_hi(ks[u][k][i]) * qs[nt][k];
-            x[nt][u][i] = fmaf(kv4_lo(ks[u][k][i]), acc[nt][i], y);
+            const uint32_t sm = T.ks[u][k][i];
+            const float y = k ? fmaf(kv4_hi(sm), qs[nt][k], x[nt][4 * u + i]) : kv4_hi(sm) * qs[nt][k];
+            x[nt][4 * u + i] = fmaf(kv4_lo(sm), acc[nt][i], y);
           }
       }
-    if (bad) {
+    // a tile that some row sees in part, or that no page holds
+    const bool part = T.bad || j0 + 32 > all_lim || (j0 < all_low && j0 + 32 > A.sinks);
+    uint32_t vis[NT];
+    if (part) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) vis[nt] = 0;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
+        const uint32_t j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
+        // scales that are not finite make their dims NaN for the rows that
+        // see the token, and reach no other row; neither do those of tokens
+        // that no row sees
+        bool odd[NG];
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) x[nt][i >> 2][i & 3] = __builtin_nanf("");
-#pragma unroll
-        for (int k = 0; k < NG; k++) vs[i >> 2][k][i & 3] = 0;
-      }
-    }
-    bool vis[NT][2][4], part[2][NG][4];
-    if (MASKED) {
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint32_t j = j0 + 16 * u + 4 * g + i;
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++) vis[nt][u][i] = j < lim[nt] && (j >= low[nt] || j < A.sinks);
+        for (int k = 0; k < NG; k++) {
+          uint32_t &sm = T.vs[i >> 2][k][i & 3];
+          odd[k] = (sm & 0x7C00u) == 0x7C00u || (sm & 0x7C000000u) == 0x7C000000u;
           const bool any = j < any_lim && (j >= any_low || j < A.sinks);
-          // what no row sees, and what is not finite, has no part in the largest scale
-#pragma unroll
-          for (int k = 0; k < NG; k++) part[u][k][i] = any && (vs[u][k][i] & 0x7C00u) != 0x7C00u;
+          sm = T.bad || odd[k] || !any ? 0 : sm;
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          const bool v = j < lim[nt] && (j >= low[nt] || j < A.sinks);
+          vis[nt] |= (uint32_t)v << i;
+          x[nt][i] = !v ? -__builtin_inff() : T.bad ? __builtin_nanf("") : x[nt][i];
+#pragma unroll
+          for (int k = 0; k < NG; k++) off[nt][k] = v && odd[k] ? __builtin_nanf("") : off[nt][k];
+        }
+      }
     }
     // does a weight times a value scale pass 2^15?
     uint32_t sm = 0;
 #pragma unroll
-    for (int u = 0; u < 2; u++)
+    for (int i = 0; i < 8; i++)
 #pragma unroll
-      for (int k = 0; k < NG; k++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint32_t b = !MASKED || part[u][k][i] ? vs[u][k][i] & 0x7FFFu : 0;
-          sm = sm > b ? sm : b;
-        }
+      for (int k = 0; k < NG; k++) {
+        const uint32_t b = T.vs[i >> 2][k][i & 3] & 0x7FFFu;
+        sm = sm > b ? sm : b;
+      }
     float m[NT];
     bool over = (sm >> 10) > e5;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-      m[nt] = -__builtin_inff();
+      m[nt] = x[nt][0];
 #pragma unroll
-      for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) m[nt] = fmaxf(m[nt], !MASKED || vis[nt][u][i] ? x[nt][u][i] : -__builtin_inff());
+      for (int i = 1; i < 8; i++) m[nt] = fmaxf(m[nt], x[nt][i]);
       over |= fmaf(cf[nt], m[nt], -ref[nt]) > (float)(29 - (int)e5);
     }
     if (__any(over)) {
@@ -593,51 +606,52 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
       for (int nt = 0; nt < NT; nt++) {
         const float mm = kv4_over_groups(m[nt], true);
         if (mm > -__builtin_inff()) top[nt] = fmaxf(top[nt], cf[nt] * mm);
-        if (top[nt] > -__builtin_inff()) {
-          const float r = top[nt] + (float)((int)e5 - 14 - 7);
-          const float a = __builtin_amdgcn_exp2f(ref[nt] - r);
-          ref[nt] = r;
-          l[nt] *= a;
+        const bool seen = top[nt] > -__builtin_inff();
+        const float r = seen ? top[nt] + (float)((int)e5 - 14 - 7) : ref[nt];
+        const float a = seen ? __builtin_amdgcn_exp2f(ref[nt] - r) : 1.0f;
+        ref[nt] = r;
+        l[nt] *= a;
 #pragma unroll
-          for (int k = 0; k < NG; k++) {
-            off[nt][k] *= a;
-            rs[nt][k] *= a;
-          }
-#pragma unroll
-          for (int k = 0; k < VH; k++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) o[nt][k][i] *= a;
+        for (int k = 0; k < NG; k++) {
+          off[nt][k] *= a;
+          rs[nt][k] *= a;
         }
+#pragma unroll
+        for (int k = 0; k < VH; k++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) o[nt][k][i] *= a;
       }
     }
     // weights, times their value scales
     uint32_t pf[NT][NG][4];
+    float p[NT][8];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-      for (int u = 0; u < 2; u++) {
-        float p[4];
+      for (int i = 0; i < 8; i++) p[nt][i] = __builtin_amdgcn_exp2f(fmaf(cf[nt], x[nt][i], -ref[nt]));
+    if (part) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          p[i] = __builtin_amdgcn_exp2f(fmaf(cf[nt], x[nt][u][i], -ref[nt]));
-          if (MASKED) p[i] = vis[nt][u][i] ? p[i] : 0.0f;
-          l[nt] += p[i];
-        }
+      for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int k = 0; k < NG; k++) {
-          float ps[4];
+        for (int i = 0; i < 8; i++) p[nt][i] = (vis[nt] >> i) & 1u ? p[nt][i] : 0.0f;
+    }
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const float s = kv4_lo(vs[u][k][i]), mid = fmaf(8.0f, s, kv4_hi(vs[u][k][i]));
-            // a row that does not see the token must not meet what it holds
-            ps[i] = !MASKED || vis[nt][u][i] ? p[i] * s : 0.0f;
-            if (!MASKED || vis[nt][u][i]) off[nt][k] = fmaf(p[i], mid, off[nt][k]);
-          }
-          pf[nt][k][2 * u] = kv4_pair(ps[0], ps[1]);
-          pf[nt][k][2 * u + 1] = kv4_pair(ps[2], ps[3]);
-          const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f};
-          rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, pf[nt][k][2 * u]), one, rs[nt][k], false);
-          rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, pf[nt][k][2 * u + 1]), one, rs[nt][k], false);
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int i = 0; i < 8; i++) l[nt] += p[nt][i];
+#pragma unroll
+    for (int k = 0; k < NG; k++)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t sa = T.vs[i >> 2][k][i & 3], sb = T.vs[i >> 2][k][(i & 3) + 1];
+        const float ma = fmaf(8.0f, kv4_lo(sa), kv4_hi(sa)), mb = fmaf(8.0f, kv4_lo(sb), kv4_hi(sb));
+        const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          const uint32_t w = kv4_pair(p[nt][i] * kv4_lo(sa), p[nt][i + 1] * kv4_lo(sb));
+          pf[nt][k][i >> 1] = w;
+          off[nt][k] = fmaf(p[nt][i + 1], mb, fmaf(p[nt][i], ma, off[nt][k]));
+          rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, w), one, rs[nt][k], false);
         }
       }
 #pragma unroll
@@ -645,8 +659,8 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
 #pragma unroll
       for (int k = 0; k < 4; k++) {
         const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu;
-        const kv4_u4 a = {(vd[0][2 * hh] >> sh) & m4, (vd[0][2 * hh + 1] >> sh) & m4, (vd[1][2 * hh] >> sh) & m4,
-                          (vd[1][2 * hh + 1] >> sh) & m4};
+        const kv4_u4 a = {(T.vd[0][2 * hh] >> sh) & m4, (T.vd[0][2 * hh + 1] >> sh) & m4, (T.vd[1][2 * hh] >> sh) & m4,
+                          (T.vd[1][2 * hh + 1] >> sh) & m4};
         const int grp = (64 * hh + 16 * k) / G;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
@@ -657,12 +671,42 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
       }
   };
 
-  for (uint32_t i = split * A.chunk + (WIDE ? 0 : wave); i < i1; i += WIDE ? 1 : 4) {
-    const uint32_t j0 = 32 * (i < tiles.head ? i : tiles.from + (i - tiles.head));
-    if (j0 + 32 <= all_lim && (j0 >= all_low || j0 + 32 <= A.sinks))
-      step(j0, kv4_bool<false>{});
-    else
-      step(j0, kv4_bool<true>{});
+  // Two tiles in registers hide the loads' latency (64 ragged sequences: 240
+  // us without, XXX with) where they do not cost the second wave of a SIMD.
+  constexpr bool AHEAD = !WIDE && 2 * (4 * KC + 16 * NG) + NT * (VH * 16 + KC * 4) <= 160;
+  constexpr uint32_t STRIDE = WIDE ? 1 : 4;
+  uint32_t i = split * A.chunk + (WIDE ? 0 : wave);
+  if (i < i1) {
+    if constexpr (!AHEAD) {
+      Tile T;
+      for (; i < i1; i += STRIDE) {
+        const uint32_t j0 = first_of(i);
+        load(T, j0, page_of(j0));
+        step(T);
+      }
+    } else {
+      // the next tile's loads, and the page of the one after, are on their way during a step
+      Tile S[2];
+      auto clamped = [&](uint32_t k) { return first_of(k < i1 ? k : i); };
+      uint32_t j0 = first_of(i);
+      load(S[0], j0, page_of(j0));
+      j0 = clamped(i + STRIDE);
+      int32_t page = page_of(j0);
+      for (;;) {
+        load(S[1], j0, page);
+        j0 = clamped(i + 2 * STRIDE);
+        page = page_of(j0);
+        step(S[0]);
+        i += STRIDE;
+        if (i >= i1) break;
+        load(S[0], j0, page);
+        j0 = clamped(i + 2 * STRIDE);
+        page = page_of(j0);
+        step(S[1]);
+        i += STRIDE;
+        if (i >= i1) break;
+      }
+    }
   }
 
   // row sums over the 4 lanes of a row; outputs without their offsets

@@ -340,6 +340,7 @@ __device__ __forceinline__ uint32_t kv4_used(uint32_t total, const Kv4Attn &A) {
 
 typedef uint32_t kv4_u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t kv4_u2 __attribute__((ext_vector_type(2)));
+typedef uint16_t kv4_s2 __attribute__((ext_vector_type(2)));
 typedef _Float16 kv4_h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 kv4_h2 __attribute__((ext_vector_type(2)));
 typedef float kv4_f4 __attribute__((ext_vector_type(4)));
@@ -351,16 +352,16 @@ __device__ __forceinline__ uint32_t kv4_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 template <int N>
-__device__ __forceinline__ void kv4_load(uint32_t (&d)[N], const uint8_t *p) {   // N dwords, 8 or more bytes aligned
+__device__ __forceinline__ void kv4_load(uint32_t (&d)[N], __amdgpu_buffer_rsrc_t r, uint32_t lane_at, uint32_t at) {
   if constexpr (N >= 4) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const kv4_u4 v = *(const kv4_u4 *)(p + 4 * i);
+      const kv4_u4 v = __builtin_amdgcn_raw_buffer_load_b128(r, lane_at + 4 * i, at, 0);
 #pragma unroll
       for (int k = 0; k < 4; k++) d[i + k] = v[k];
     }
   } else {
-    const kv4_u2 v = *(const kv4_u2 *)p;
+    const kv4_u2 v = __builtin_amdgcn_raw_buffer_load_b64(r, lane_at, at, 0);
     d[0] = v[0];
     d[1] = v[1];
   }
@@ -401,8 +402,14 @@ __device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over 
 //
 // WIDE: the 4 waves of a workgroup take different rows and every tile.
 // Otherwise they share rows, take every 4th tile and join their sums.
+// waves of a SIMD that the registers leave room for
 template <int D, int G, int NT, bool WIDE>
-__global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B, Kv4Attn A) {
+constexpr int kv4_waves() {
+  return D == 256 || (D == 128 && NT == 2 && (G == 32 || !WIDE)) ? 1 : 2;
+}
+
+template <int D, int G, int NT, bool WIDE>
+__global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attention_kernel(Kv4View C, Kv4Rows B, Kv4Attn A) {
   constexpr int NG = D / G, KC = D / 32, VH = D / 64;
   constexpr int CPG = G / 32;                        // score products of a group
   constexpr int VALS = NT * VH * 4;                  // output registers of 4
@@ -486,38 +493,43 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
   const uint32_t all_low = A.window && any_lim > A.window ? any_lim - A.window : 0;
   const uint32_t any_low = A.window && all_lim > A.window ? all_lim - A.window : 0;
   uint32_t e5 = 0;                                   // exponent field of the largest value scale so far
-  const uint32_t mask = (1u << C.page_shift) - 1;
-
   // the first token of the i-th tile, and its page (-1: none)
-  auto first_of = [&](uint32_t i) { return 32 * (i < tiles.head ? i : tiles.from + (i - tiles.head)); };
+  const uint32_t jump = 32 * (tiles.from - tiles.head);
+  auto first_of = [&](uint32_t i) { return 32 * i + (i < tiles.head ? 0 : jump); };
+  const int32_t *table = B.table + (uint64_t)seq * B.max_pages;
   auto page_of = [&](uint32_t j0) {
     const uint32_t pi = j0 >> C.page_shift;
-    const int32_t page = pi < B.max_pages ? B.table[(uint64_t)seq * B.max_pages + pi] : -1;
-    return page >= 0 && (uint64_t)page < C.n_pages ? page : -1;
+    return pi < B.max_pages ? table[pi] : -1;
   };
 
+  // Buffer loads: the block's address and the tile's offset are in scalar
+  // registers, a lane's offsets never change, and nothing past the block is
+  // read.
   struct Tile {
     uint32_t j0;
     bool bad;
     uint32_t kd[2][KC], vd[2][2 * VH], ks[2][NG][4], vs[2][NG][4];
   };
+  const uint32_t ps = C.page_shift, n_pages = (uint32_t)C.n_pages;
+  uint8_t *head0 = C.pages + (uint64_t)h * ((uint32_t)(D + 8 * NG) << ps);
+  const uint32_t k_at = n * (D / 2) + g * (D / 8), v_at = lane * (D / 8), s_at = 16 * g;
   auto load = [&](Tile &T, uint32_t j0, int32_t page) {
     T.j0 = j0;
-    T.bad = page < 0;
-    const uint32_t slot = j0 & mask;
-    const uint8_t *blk = kv4_block(C, T.bad ? 0u : (uint32_t)page, h);
-    const uint8_t *vblk = blk + C.kc + C.sc;
+    T.bad = (uint32_t)page >= n_pages;                // negative ids too: there are fewer than 2^31 pages
+    const uint32_t slot = j0 & ((1u << ps) - 1), bytes = (uint32_t)(D + 8 * NG) << ps;   // of a page and head
+    const uint64_t at = (uint64_t)((T.bad ? 0u : (uint32_t)page) * (uint64_t)C.kv_heads) * bytes;
+    const auto blk = __builtin_amdgcn_make_buffer_rsrc(head0 + at, 0, (int)bytes, 0x00020000);
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      kv4_load(T.kd[u], blk + (slot + 16 * u + n) * (D / 2) + g * (D / 8));
+    for (int w = 0; w < 2; w++) {
+      const uint32_t part = (uint32_t)(w * (D / 2 + 4 * NG)) << ps;
+      const uint32_t codes = part + slot * (D / 2), scales = part + ((D / 2) << ps) + slot * 4;
 #pragma unroll
-      for (int k = 0; k < NG; k++) kv4_load(T.ks[u][k], blk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
-    }
+      for (int u = 0; u < 2; u++) {
+        kv4_load(w ? T.vd[u] : T.kd[u], blk, (w ? v_at : k_at) + 16 * u * (D / 2), codes);
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      kv4_load(T.vd[u], vblk + (slot + 16 * u) * (D / 2) + lane * (D / 8));
-#pragma unroll
-      for (int k = 0; k < NG; k++) kv4_load(T.vs[u][k], vblk + C.kc + kv4_scale(C, slot + 16 * u + 4 * g, k));
+        for (int k = 0; k < NG; k++)
+          kv4_load(w ? T.vs[u][k] : T.ks[u][k], blk, s_at + 64 * u, scales + ((uint32_t)(4 * k) << ps));
+      }
     }
   };
 
@@ -549,43 +561,57 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
       }
     // a tile that some row sees in part, or that no page holds
     const bool part = T.bad || j0 + 32 > all_lim || (j0 < all_low && j0 + 32 > A.sinks);
-    uint32_t vis[NT];
+    uint32_t vis[NT];                                // bit i: row n sees the lane's token i
     if (part) {
+      if (T.bad) {
 #pragma unroll
-      for (int nt = 0; nt < NT; nt++) vis[nt] = 0;
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const uint32_t j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-        // scales that are not finite make their dims NaN for the rows that
-        // see the token, and reach no other row; neither do those of tokens
-        // that no row sees
-        bool odd[NG];
+          for (int i = 0; i < 8; i++) x[nt][i] = __builtin_nanf("");
+      }
+      auto below = [&](uint32_t limit) {             // bit i: the lane's token i is below limit
+        auto four = [&](uint32_t base) {
+          const int c = (int)(limit - base);
+          return (1u << (c < 0 ? 0 : c > 4 ? 4 : c)) - 1;
+        };
+        return four(j0 + 4 * g) | four(j0 + 16 + 4 * g) << 4;
+      };
+      const uint32_t first = below(A.sinks < 0x7FFFFFFFu ? A.sinks : 0x7FFFFFFFu);
+      // Scales that are not finite make their dims NaN for the rows that see
+      // the token, and reach no other row; nor do those of tokens that no row
+      // sees.
+      const uint32_t any = T.bad ? 0 : below(any_lim) & (~below(any_low) | first);
+      uint32_t odd[NG];
 #pragma unroll
-        for (int k = 0; k < NG; k++) {
+      for (int k = 0; k < NG; k++) {
+        odd[k] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
           uint32_t &sm = T.vs[i >> 2][k][i & 3];
-          odd[k] = (sm & 0x7C00u) == 0x7C00u || (sm & 0x7C000000u) == 0x7C000000u;
-          const bool any = j < any_lim && (j >= any_low || j < A.sinks);
-          sm = T.bad || odd[k] || !any ? 0 : sm;
+          const uint32_t c = (sm & 0x7C00u) == 0x7C00u || (sm & 0x7C000000u) == 0x7C000000u;
+          odd[k] |= c << i;
+          sm = (any >> i) & ~c & 1u ? sm : 0;
         }
+      }
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          const bool v = j < lim[nt] && (j >= low[nt] || j < A.sinks);
-          vis[nt] |= (uint32_t)v << i;
-          x[nt][i] = !v ? -__builtin_inff() : T.bad ? __builtin_nanf("") : x[nt][i];
+      for (int nt = 0; nt < NT; nt++) {
+        vis[nt] = below(lim[nt]) & (~below(low[nt]) | first);
 #pragma unroll
-          for (int k = 0; k < NG; k++) off[nt][k] = v && odd[k] ? __builtin_nanf("") : off[nt][k];
-        }
+        for (int i = 0; i < 8; i++) x[nt][i] = (vis[nt] >> i) & 1u ? x[nt][i] : -__builtin_inff();
+#pragma unroll
+        for (int k = 0; k < NG; k++) off[nt][k] = vis[nt] & odd[k] ? __builtin_nanf("") : off[nt][k];
       }
     }
     // does a weight times a value scale pass 2^15?
-    uint32_t sm = 0;
+    kv4_s2 sm2 = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
       for (int k = 0; k < NG; k++) {
-        const uint32_t b = T.vs[i >> 2][k][i & 3] & 0x7FFFu;
-        sm = sm > b ? sm : b;
+        // halves apart: the scale's bits are the low ones
+        sm2 = __builtin_elementwise_max(sm2, __builtin_bit_cast(kv4_s2, T.vs[i >> 2][k][i & 3]));
       }
+    const uint32_t sm = __builtin_bit_cast(uint32_t, sm2) & 0x7FFFu;
     float m[NT];
     bool over = (sm >> 10) > e5;
 #pragma unroll
@@ -673,7 +699,7 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4View C, Kv4Rows B
 
   // Two tiles in registers hide the loads' latency (64 ragged sequences: 240
   // us without, XXX with) where they do not cost the second wave of a SIMD.
-  constexpr bool AHEAD = !WIDE && 2 * (4 * KC + 16 * NG) + NT * (VH * 16 + KC * 4) <= 160;
+  constexpr bool AHEAD = 2 * (4 * KC + 16 * NG) + NT * (VH * 16 + KC * 4) <= 160;
   constexpr uint32_t STRIDE = WIDE ? 1 : 4;
   uint32_t i = split * A.chunk + (WIDE ? 0 : wave);
   if (i < i1) {

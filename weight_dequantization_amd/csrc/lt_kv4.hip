@@ -52,7 +52,7 @@ lt_status launched() { return hipGetLastError() == hipSuccess ? LT_OK : LT_ERR_L
 // host alone (so that the workspace can be asked for ahead).
 struct Plan {
   bool wide;                 // waves over rows, not over tiles
-  uint32_t nt, unit, row_blocks, chunk, splits;
+  uint32_t nt, unit, row_blocks, chunk_shift, splits;
   uint64_t bytes;
 };
 
@@ -76,11 +76,12 @@ Plan plan_of(const lt::Kv4View &C, const lt::Kv4Rows &B, uint64_t max_q, uint64_
   if (p.wide) {
     if (units < 256) chunk = (units * tiles + 511) / 512 < 32 ? 32 : (units * tiles + 511) / 512;
   } else if (tiles > 16) {
-    chunk = (units * tiles + 1023) / 1024;
-    chunk = chunk < 16 ? 16 : chunk > 64 ? 64 : chunk;
+    chunk = (units * tiles + 511) / 512;
+    chunk = chunk < 16 ? 16 : chunk > 128 ? 128 : chunk;
   }
-  p.chunk = (uint32_t)((chunk + 3) / 4 * 4);
-  p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
+  p.chunk_shift = 0;
+  while ((1ull << p.chunk_shift) < chunk) p.chunk_shift++;
+  p.splits = (uint32_t)((tiles + (1ull << p.chunk_shift) - 1) >> p.chunk_shift);
   p.bytes = p.splits > 1 ? (uint64_t)B.n_tokens * C.kv_heads * ratio * p.splits * (C.dim + 2) * 4 : 0;
   return p;
 }
@@ -220,8 +221,7 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
   if (!(scale > -3.4e38f && scale < 3.4e38f)) return LT_ERR_INVALID_ARG;
   const Plan p = plan_of(C, B, batch->max_q_len, batch->max_kv_len, heads / C.kv_heads, window, sinks);
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return LT_ERR_INVALID_ARG;
-  const uint64_t blocks = (uint64_t)B.n_seqs * C.kv_heads * p.row_blocks * p.splits;
-  if (heads > 65535 || blocks > 0x7FFFFFFFull || (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
+  if (heads > 65535 || B.n_seqs > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 || (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
       (uint64_t)batch->max_q_len * (heads / C.kv_heads) > 0x7FFFFFFFull)
     return LT_ERR_UNSUPPORTED;
   if (B.n_tokens == 0 || B.n_seqs == 0 || batch->max_q_len == 0) return LT_OK;
@@ -240,12 +240,12 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
   A.sinks = sinks;
   A.max_q = batch->max_q_len;
   A.row_blocks = p.row_blocks;
-  A.chunk = p.chunk;
+  A.chunk_shift = p.chunk_shift;
   A.splits = p.splits;
   A.part_o = (float *)workspace;
   A.part_ml = p.bytes ? (float *)workspace + (uint64_t)B.n_tokens * heads * p.splits * C.dim : nullptr;
   A.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid((uint32_t)blocks);
+  const dim3 grid(C.kv_heads, B.n_seqs, p.row_blocks * p.splits);
   hipStream_t s = (hipStream_t)stream;
   switch (C.dim * 1024 + C.group) {
     case 64 * 1024 + 32: launch_attention<64, 32>(p, grid, s, C, B, A); break;

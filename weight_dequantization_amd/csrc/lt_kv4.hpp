@@ -311,7 +311,7 @@ struct Kv4Attn {
   int64_t q_ts, q_hs, o_ts, o_hs;
   uint32_t heads, ratio, bf16, window, sinks, max_q;
   uint32_t row_blocks;       // workgroups over the rows of a sequence and kv head
-  uint32_t chunk, splits;    // 32-token tiles a workgroup takes, workgroups over a row's tiles
+  uint32_t chunk_shift, splits;   // log2 of the 32-token tiles a workgroup takes; workgroups over a row's tiles
   float *part_o, *part_ml;   // [n_tokens * heads][splits][dim], [..][2]: sums, reference and weight
   float scale_log2;          // scale * log2(e)
 };
@@ -334,7 +334,7 @@ __device__ __forceinline__ Kv4Tiles kv4_tiles(int32_t p0, int32_t p1, uint32_t w
   return t;
 }
 __device__ __forceinline__ uint32_t kv4_used(uint32_t total, const Kv4Attn &A) {
-  const uint32_t n = (total + A.chunk - 1) / A.chunk;
+  const uint32_t n = (total + (1u << A.chunk_shift) - 1) >> A.chunk_shift;
   return n < 1 ? 1 : n < A.splits ? n : A.splits;
 }
 
@@ -400,8 +400,10 @@ __device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over 
 // the largest value scale so far would pass 2^15, and is then set so that it
 // is 2^7 (fp16 keeps 11 bits down to 2^-14).
 //
-// WIDE: the 4 waves of a workgroup take different rows and every tile.
-// Otherwise they share rows, take every 4th tile and join their sums.
+// WIDE: the 4 waves of a workgroup take different rows and every tile (one
+// wave a workgroup: 751 us for prompt chunks against 721, they share what
+// they load).  Otherwise they share rows, take every 4th tile and join their
+// sums.
 // waves of a SIMD that the registers leave room for
 template <int D, int G, int NT, bool WIDE>
 constexpr int kv4_waves() {
@@ -413,15 +415,14 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   constexpr int NG = D / G, KC = D / 32, VH = D / 64;
   constexpr int CPG = G / 32;                        // score products of a group
   constexpr int VALS = NT * VH * 4;                  // output registers of 4
-  __shared__ kv4_f4 join_o[WIDE ? 1 : 3][WIDE ? 1 : VALS][64];
-  __shared__ float join_ml[WIDE ? 1 : 3][WIDE ? 1 : NT][2][16];
+  constexpr int JOIN = VH * 4 < 8 ? VH * 4 : 8;       // of them joined at a time
+  __shared__ kv4_f4 join_o[WIDE ? 1 : 4][WIDE ? 1 : JOIN][64];
+  __shared__ float join_ml[WIDE ? 1 : 4][WIDE ? 1 : NT][2][16];
   const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t pairs = B.n_seqs * C.kv_heads;
-  const uint32_t pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
   // late rows see the most tokens: they start first
-  const uint32_t rb = A.row_blocks - 1 - rest % A.row_blocks, split = rest / A.row_blocks;
-  const uint32_t seq = pair / C.kv_heads, h = pair % C.kv_heads;
+  const uint32_t h = blockIdx.x, seq = blockIdx.y, split = A.row_blocks > 1 ? blockIdx.z / A.row_blocks : blockIdx.z;
+  const uint32_t rb = A.row_blocks - 1 - (blockIdx.z - split * A.row_blocks);
   const int32_t q0 = B.q_start[seq], q1 = B.q_start[seq + 1];
   const int32_t kvl = B.kv_len[seq] > 0 ? B.kv_len[seq] : 0;
   if (q0 < 0 || q1 <= q0 || (uint32_t)q1 > B.n_tokens) return;
@@ -435,7 +436,56 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   const Kv4Tiles tiles = kv4_tiles(p_first, p_last, A.window, A.sinks);
   const uint32_t used = kv4_used(tiles.total, A);
   if (split >= used) return;
-  const uint32_t i1 = split + 1 == A.splits || (split + 1) * A.chunk > tiles.total ? tiles.total : (split + 1) * A.chunk;
+  const uint32_t i0 = split << A.chunk_shift;
+  const uint32_t i1 = split + 1 == A.splits || tiles.total - i0 < (1u << A.chunk_shift) ? tiles.total
+                                                                                      : i0 + (1u << A.chunk_shift);
+
+  // the first token of the i-th tile, and its page (-1: none)
+  const uint32_t jump = 32 * (tiles.from - tiles.head);
+  auto first_of = [&](uint32_t i) { return 32 * i + (i < tiles.head ? 0 : jump); };
+  const int32_t *table = B.table + (uint64_t)seq * B.max_pages;
+  auto page_of = [&](uint32_t j0) {
+    const uint32_t pi = j0 >> C.page_shift;
+    return pi < B.max_pages ? table[pi] : -1;
+  };
+
+  // Buffer loads: the block's address and the tile's offset are in scalar
+  // registers, a lane's offsets never change, and nothing past the block is
+  // read.
+  uint32_t kd[2][KC], vd[2][2 * VH], ks[2][NG][4], vs[2][NG][4];
+  const uint32_t ps = C.page_shift, n_pages = (uint32_t)C.n_pages;
+  uint8_t *head0 = C.pages + (uint64_t)h * ((uint32_t)(D + 8 * NG) << ps);
+  const uint32_t k_at = n * (D / 2) + g * (D / 8), v_at = lane * (D / 8), s_at = 16 * g;
+  auto block_of = [&](int32_t page) {                // ids that are none, negative ones too: page 0, never used
+    const uint32_t bytes = (uint32_t)(D + 8 * NG) << ps;
+    const uint64_t at = (uint64_t)((uint32_t)page < n_pages ? (uint32_t)page : 0u) * C.kv_heads * bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(head0 + at, 0, (int)bytes, 0x00020000);
+  };
+  auto load_codes = [&](uint32_t j0, int32_t page, bool value) {
+    const uint32_t slot = j0 & ((1u << ps) - 1), part = value ? (uint32_t)(D / 2 + 4 * NG) << ps : 0;
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+      kv4_load(value ? vd[u] : kd[u], block_of(page), (value ? v_at : k_at) + 16 * u * (D / 2), part + slot * (D / 2));
+  };
+  auto load_scales = [&](uint32_t j0, int32_t page, bool value) {
+    const uint32_t slot = j0 & ((1u << ps) - 1), part = (uint32_t)(D / 2 + (value ? D / 2 + 4 * NG : 0)) << ps;
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int k = 0; k < NG; k++)
+        kv4_load(value ? vs[u][k] : ks[u][k], block_of(page), s_at + 64 * u, part + slot * 4 + ((uint32_t)(4 * k) << ps));
+  };
+
+  // the first tile is on its way while the queries are prepared
+  constexpr uint32_t STRIDE = WIDE ? 1 : 4;
+  uint32_t i = i0 + (WIDE ? 0 : wave);
+  auto tile_of = [&](uint32_t k) { return first_of(k < i1 ? k : i); };   // past the end: loads that nothing uses
+  uint32_t j0 = first_of(i), j1 = tile_of(i + STRIDE);
+  int32_t page0 = page_of(j0), page1 = page_of(j1);
+  load_codes(j0, page0, false);
+  load_scales(j0, page0, false);
+  load_scales(j0, page0, true);
+  load_codes(j0, page0, true);
 
   // the rows' queries, limits and softmax state
   kv4_h8 qf[NT][KC];
@@ -451,29 +501,51 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
     lim[nt] = p < 0 ? 0 : (uint32_t)p + 1;
     low[nt] = A.window && lim[nt] > A.window ? lim[nt] - A.window : 0;
     const uint16_t *src = A.q + (int64_t)(q0 + (int32_t)t) * A.q_ts + (int64_t)hd * A.q_hs + 8 * g;
+    kv4_u4 raw[KC];
     float v[KC][8], most = 0.0f;
 #pragma unroll
-    for (int c = 0; c < KC; c++) {
-      load8(src + 32 * c, A.bf16 != 0, v[c]);
+    for (int c = 0; c < KC; c++) raw[c] = *(const kv4_u4 *)(src + 32 * c);
+    if (A.bf16) {
+#pragma unroll
+      for (int c = 0; c < KC; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          v[c][i] = f32_of_bf16((uint16_t)raw[c][i / 2]);
+          v[c][i + 1] = __builtin_bit_cast(float, (uint32_t)(raw[c][i / 2] & 0xFFFF0000u));
+        }
+    } else {
+#pragma unroll
+      for (int c = 0; c < KC; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          v[c][i] = kv4_lo(raw[c][i / 2]);
+          v[c][i + 1] = kv4_hi(raw[c][i / 2]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < KC; c++)
 #pragma unroll
       for (int i = 0; i < 8; i++) most = fmaxf(most, fabsf(v[c][i]));
-    }
     most = kv4_over_groups(most, true);
-    const int e = most > 0.0f ? 12 - ((int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127) : 0;
-    cf[nt] = ldexpf(fabsf(A.scale_log2), 24 - e);
-    const float sign = A.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    int e = most > 0.0f ? 12 - ((int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127) : 0;
+    e = e < 126 ? e : 126;
+    cf[nt] = fmaxf(ldexpf(fabsf(A.scale_log2), 24 - e), 1e-37f);   // not 0: 0 times -inf is none
+    const float mult = __builtin_bit_cast(float, (uint32_t)(e + 127) << 23 | (A.scale_log2 < 0.0f ? 0x80000000u : 0u));
+    const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f}, d16 = {(_Float16)0.0625f, (_Float16)0.0625f};
 #pragma unroll
     for (int k = 0; k < NG; k++) qs[nt][k] = 0.0f;
 #pragma unroll
     for (int c = 0; c < KC; c++) {
-      _Float16 w[8];
+      kv4_u4 w;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        w[i] = (_Float16)(ldexpf(v[c][i], e) * sign);
-        qs[nt][c / CPG] += (float)w[i];
+      for (int i = 0; i < 4; i++) {
+        const uint32_t two = kv4_pair(v[c][i] * mult, v[c][i + 4] * mult);
+        kv4_h2 t2 = __builtin_bit_cast(kv4_h2, two);
+        qs[nt][c / CPG] = __builtin_amdgcn_fdot2(t2, one, qs[nt][c / CPG], false);
+        if (i & 1) t2 *= d16;
+        w[i] = __builtin_bit_cast(uint32_t, t2);
       }
-      const _Float16 d16 = (_Float16)0.0625f;
-      qf[nt][c] = kv4_h8{w[0], w[4], w[1] * d16, w[5] * d16, w[2], w[6], w[3] * d16, w[7] * d16};
+      qf[nt][c] = __builtin_bit_cast(kv4_h8, w);
     }
 #pragma unroll
     for (int k = 0; k < NG; k++) {
@@ -493,245 +565,191 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   const uint32_t all_low = A.window && any_lim > A.window ? any_lim - A.window : 0;
   const uint32_t any_low = A.window && all_lim > A.window ? all_lim - A.window : 0;
   uint32_t e5 = 0;                                   // exponent field of the largest value scale so far
-  // the first token of the i-th tile, and its page (-1: none)
-  const uint32_t jump = 32 * (tiles.from - tiles.head);
-  auto first_of = [&](uint32_t i) { return 32 * i + (i < tiles.head ? 0 : jump); };
-  const int32_t *table = B.table + (uint64_t)seq * B.max_pages;
-  auto page_of = [&](uint32_t j0) {
-    const uint32_t pi = j0 >> C.page_shift;
-    return pi < B.max_pages ? table[pi] : -1;
-  };
-
-  // Buffer loads: the block's address and the tile's offset are in scalar
-  // registers, a lane's offsets never change, and nothing past the block is
-  // read.
-  struct Tile {
-    uint32_t j0;
-    bool bad;
-    uint32_t kd[2][KC], vd[2][2 * VH], ks[2][NG][4], vs[2][NG][4];
-  };
-  const uint32_t ps = C.page_shift, n_pages = (uint32_t)C.n_pages;
-  uint8_t *head0 = C.pages + (uint64_t)h * ((uint32_t)(D + 8 * NG) << ps);
-  const uint32_t k_at = n * (D / 2) + g * (D / 8), v_at = lane * (D / 8), s_at = 16 * g;
-  auto load = [&](Tile &T, uint32_t j0, int32_t page) {
-    T.j0 = j0;
-    T.bad = (uint32_t)page >= n_pages;                // negative ids too: there are fewer than 2^31 pages
-    const uint32_t slot = j0 & ((1u << ps) - 1), bytes = (uint32_t)(D + 8 * NG) << ps;   // of a page and head
-    const uint64_t at = (uint64_t)((T.bad ? 0u : (uint32_t)page) * (uint64_t)C.kv_heads) * bytes;
-    const auto blk = __builtin_amdgcn_make_buffer_rsrc(head0 + at, 0, (int)bytes, 0x00020000);
-#pragma unroll
-    for (int w = 0; w < 2; w++) {
-      const uint32_t part = (uint32_t)(w * (D / 2 + 4 * NG)) << ps;
-      const uint32_t codes = part + slot * (D / 2), scales = part + ((D / 2) << ps) + slot * 4;
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-        kv4_load(w ? T.vd[u] : T.kd[u], blk, (w ? v_at : k_at) + 16 * u * (D / 2), codes);
-#pragma unroll
-        for (int k = 0; k < NG; k++)
-          kv4_load(w ? T.vs[u][k] : T.ks[u][k], blk, s_at + 64 * u, scales + ((uint32_t)(4 * k) << ps));
-      }
-    }
-  };
-
-  auto step = [&](Tile &T) {
-    const uint32_t j0 = T.j0;
-    float x[NT][8];
+  // K's products with the queries, and the scores out of them
+  kv4_f4 acc[NT][2][NG];
+  float x[NT][8];
+  auto products = [&]() {
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
-      for (int k = 0; k < NG; k++) {
-        kv4_f4 acc[NT];
-#pragma unroll
-        for (int c = k * CPG; c < (k + 1) * CPG; c++) {
-          const uint32_t w = T.kd[u][c], w8 = w >> 8;
-          const kv4_u4 a = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++)
-            acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(kv4_h8, a), qf[nt][c],
-                                                             c % CPG ? acc[nt] : kv4_f4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-        }
+      for (int c = 0; c < KC; c++) {
+        const uint32_t w = kd[u][c], w8 = w >> 8;
+        const kv4_u4 a = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const uint32_t sm = T.ks[u][k][i];
-            const float y = k ? fmaf(kv4_hi(sm), qs[nt][k], x[nt][4 * u + i]) : kv4_hi(sm) * qs[nt][k];
-            x[nt][4 * u + i] = fmaf(kv4_lo(sm), acc[nt][i], y);
-          }
+          acc[nt][u][c / CPG] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              __builtin_bit_cast(kv4_h8, a), qf[nt][c], c % CPG ? acc[nt][u][c / CPG] : kv4_f4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
       }
-    // a tile that some row sees in part, or that no page holds
-    const bool part = T.bad || j0 + 32 > all_lim || (j0 < all_low && j0 + 32 > A.sinks);
-    uint32_t vis[NT];                                // bit i: row n sees the lane's token i
-    if (part) {
-      if (T.bad) {
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int i = 0; i < 8; i++) x[nt][i] = __builtin_nanf("");
-      }
-      auto below = [&](uint32_t limit) {             // bit i: the lane's token i is below limit
-        auto four = [&](uint32_t base) {
-          const int c = (int)(limit - base);
-          return (1u << (c < 0 ? 0 : c > 4 ? 4 : c)) - 1;
-        };
-        return four(j0 + 4 * g) | four(j0 + 16 + 4 * g) << 4;
-      };
-      const uint32_t first = below(A.sinks < 0x7FFFFFFFu ? A.sinks : 0x7FFFFFFFu);
-      // Scales that are not finite make their dims NaN for the rows that see
-      // the token, and reach no other row; nor do those of tokens that no row
-      // sees.
-      const uint32_t any = T.bad ? 0 : below(any_lim) & (~below(any_low) | first);
-      uint32_t odd[NG];
-#pragma unroll
-      for (int k = 0; k < NG; k++) {
-        odd[k] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          uint32_t &sm = T.vs[i >> 2][k][i & 3];
-          const uint32_t c = (sm & 0x7C00u) == 0x7C00u || (sm & 0x7C000000u) == 0x7C000000u;
-          odd[k] |= c << i;
-          sm = (any >> i) & ~c & 1u ? sm : 0;
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++) {
-        vis[nt] = below(lim[nt]) & (~below(low[nt]) | first);
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[nt][i] = (vis[nt] >> i) & 1u ? x[nt][i] : -__builtin_inff();
-#pragma unroll
-        for (int k = 0; k < NG; k++) off[nt][k] = vis[nt] & odd[k] ? __builtin_nanf("") : off[nt][k];
-      }
-    }
-    // does a weight times a value scale pass 2^15?
-    kv4_s2 sm2 = {0, 0};
+  };
+  auto scores = [&]() {
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
       for (int k = 0; k < NG; k++) {
-        // halves apart: the scale's bits are the low ones
-        sm2 = __builtin_elementwise_max(sm2, __builtin_bit_cast(kv4_s2, T.vs[i >> 2][k][i & 3]));
-      }
-    const uint32_t sm = __builtin_bit_cast(uint32_t, sm2) & 0x7FFFu;
-    float m[NT];
-    bool over = (sm >> 10) > e5;
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++) {
-      m[nt] = x[nt][0];
-#pragma unroll
-      for (int i = 1; i < 8; i++) m[nt] = fmaxf(m[nt], x[nt][i]);
-      over |= fmaf(cf[nt], m[nt], -ref[nt]) > (float)(29 - (int)e5);
-    }
-    if (__any(over)) {
-      uint32_t s5 = sm >> 10;
-      uint32_t t = (uint32_t)__shfl_xor((int)s5, 16);
-      s5 = s5 > t ? s5 : t;
-      t = (uint32_t)__shfl_xor((int)s5, 32);
-      s5 = s5 > t ? s5 : t;
-      e5 = __builtin_amdgcn_readfirstlane(e5 > s5 ? e5 : s5);
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++) {
-        const float mm = kv4_over_groups(m[nt], true);
-        if (mm > -__builtin_inff()) top[nt] = fmaxf(top[nt], cf[nt] * mm);
-        const bool seen = top[nt] > -__builtin_inff();
-        const float r = seen ? top[nt] + (float)((int)e5 - 14 - 7) : ref[nt];
-        const float a = seen ? __builtin_amdgcn_exp2f(ref[nt] - r) : 1.0f;
-        ref[nt] = r;
-        l[nt] *= a;
-#pragma unroll
-        for (int k = 0; k < NG; k++) {
-          off[nt][k] *= a;
-          rs[nt][k] *= a;
-        }
-#pragma unroll
-        for (int k = 0; k < VH; k++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) o[nt][k][i] *= a;
-      }
-    }
-    // weights, times their value scales
-    uint32_t pf[NT][NG][4];
-    float p[NT][8];
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-      for (int i = 0; i < 8; i++) p[nt][i] = __builtin_amdgcn_exp2f(fmaf(cf[nt], x[nt][i], -ref[nt]));
-    if (part) {
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) p[nt][i] = (vis[nt] >> i) & 1u ? p[nt][i] : 0.0f;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-      for (int i = 0; i < 8; i++) l[nt] += p[nt][i];
-#pragma unroll
-    for (int k = 0; k < NG; k++)
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const uint32_t sa = T.vs[i >> 2][k][i & 3], sb = T.vs[i >> 2][k][(i & 3) + 1];
-        const float ma = fmaf(8.0f, kv4_lo(sa), kv4_hi(sa)), mb = fmaf(8.0f, kv4_lo(sb), kv4_hi(sb));
-        const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+        const uint32_t sm = ks[i >> 2][k][i & 3];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
-          const uint32_t w = kv4_pair(p[nt][i] * kv4_lo(sa), p[nt][i + 1] * kv4_lo(sb));
-          pf[nt][k][i >> 1] = w;
-          off[nt][k] = fmaf(p[nt][i + 1], mb, fmaf(p[nt][i], ma, off[nt][k]));
-          rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, w), one, rs[nt][k], false);
-        }
-      }
-#pragma unroll
-    for (int hh = 0; hh < VH; hh++)
-#pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu;
-        const kv4_u4 a = {(T.vd[0][2 * hh] >> sh) & m4, (T.vd[0][2 * hh + 1] >> sh) & m4, (T.vd[1][2 * hh] >> sh) & m4,
-                          (T.vd[1][2 * hh + 1] >> sh) & m4};
-        const int grp = (64 * hh + 16 * k) / G;
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          const kv4_u4 pb = {pf[nt][grp][0], pf[nt][grp][1], pf[nt][grp][2], pf[nt][grp][3]};
-          o[nt][hh][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(kv4_h8, a), __builtin_bit_cast(kv4_h8, pb),
-                                                                o[nt][hh][k], 0, 0, 0);
+          const float y = k ? fmaf(kv4_hi(sm), qs[nt][k], x[nt][i]) : kv4_hi(sm) * qs[nt][k];
+          x[nt][i] = fmaf(kv4_lo(sm), acc[nt][i >> 2][k][i & 3], y);
         }
       }
   };
+  // a tile that some row sees in part, or that no page holds
+  auto limit_to_seen = [&](uint32_t j0, bool bad) {
+    auto below = [&](uint32_t limit) {               // bit i: the lane's token i is below limit
+      auto four = [&](uint32_t base) {
+        const int c = (int)(limit - base);
+        return (1u << (c < 0 ? 0 : c > 4 ? 4 : c)) - 1;
+      };
+      return four(j0 + 4 * g) | four(j0 + 16 + 4 * g) << 4;
+    };
+    const uint32_t first = below(A.sinks < 0x7FFFFFFFu ? A.sinks : 0x7FFFFFFFu);
+    // Scales that are not finite make their dims NaN for the rows that see
+    // the token, and reach no other row; nor do those of tokens that no row
+    // sees.
+    const uint32_t any = bad ? 0 : below(any_lim) & (~below(any_low) | first);
+    uint32_t odd[NG];
+#pragma unroll
+    for (int k = 0; k < NG; k++) {
+      odd[k] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        uint32_t &sm = vs[i >> 2][k][i & 3];
+        const uint32_t c = (sm & 0x7C00u) == 0x7C00u || (sm & 0x7C000000u) == 0x7C000000u;
+        odd[k] |= c << i;
+        sm = (any >> i) & ~c & 1u ? sm : 0;
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const uint32_t vis = below(lim[nt]) & (~below(low[nt]) | first);
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        x[nt][i] = (vis >> i) & 1u ? (bad ? __builtin_nanf("") : x[nt][i]) : -__builtin_inff();
+#pragma unroll
+      for (int k = 0; k < NG; k++) off[nt][k] = vis & odd[k] && !bad ? __builtin_nanf("") : off[nt][k];
+    }
+  };
 
-  // Two tiles in registers hide the loads' latency (64 ragged sequences: 240
-  // us without, XXX with) where they do not cost the second wave of a SIMD.
-  constexpr bool AHEAD = 2 * (4 * KC + 16 * NG) + NT * (VH * 16 + KC * 4) <= 160;
-  constexpr uint32_t STRIDE = WIDE ? 1 : 4;
-  uint32_t i = split * A.chunk + (WIDE ? 0 : wave);
+  // Steps overlap: while one tile's weights are made and multiplied with its
+  // values, the next tile's scores are multiplied, and each register's next
+  // load is on its way as soon as it has been used.
   if (i < i1) {
-    if constexpr (!AHEAD) {
-      Tile T;
-      for (; i < i1; i += STRIDE) {
-        const uint32_t j0 = first_of(i);
-        load(T, j0, page_of(j0));
-        step(T);
+    products();
+    load_codes(j1, page1, false);
+    scores();
+    load_scales(j1, page1, false);
+    for (;;) {
+      const uint32_t j2 = tile_of(i + 2 * STRIDE);
+      const int32_t page2 = page_of(j2);
+      const bool bad = (uint32_t)page0 >= n_pages;
+      if (bad || j0 + 32 > all_lim || (j0 < all_low && j0 + 32 > A.sinks)) limit_to_seen(j0, bad);
+      // does a weight times a value scale pass 2^15?
+      kv4_s2 sm2 = {0, 0};
+#pragma unroll
+      for (int t = 0; t < 8; t++)
+#pragma unroll
+        for (int k = 0; k < NG; k++)                 // halves apart: the scale's bits are the low ones
+          sm2 = __builtin_elementwise_max(sm2, __builtin_bit_cast(kv4_s2, vs[t >> 2][k][t & 3]));
+      const uint32_t sm = __builtin_bit_cast(uint32_t, sm2) & 0x7FFFu;
+      float m[NT];
+      bool over = (sm >> 10) > e5;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        m[nt] = x[nt][0];
+#pragma unroll
+        for (int t = 1; t < 8; t++) m[nt] = fmaxf(m[nt], x[nt][t]);
+        over |= fmaf(cf[nt], m[nt], -ref[nt]) > (float)(29 - (int)e5);
       }
-    } else {
-      // the next tile's loads, and the page of the one after, are on their way during a step
-      Tile S[2];
-      auto clamped = [&](uint32_t k) { return first_of(k < i1 ? k : i); };
-      uint32_t j0 = first_of(i);
-      load(S[0], j0, page_of(j0));
-      j0 = clamped(i + STRIDE);
-      int32_t page = page_of(j0);
-      for (;;) {
-        load(S[1], j0, page);
-        j0 = clamped(i + 2 * STRIDE);
-        page = page_of(j0);
-        step(S[0]);
-        i += STRIDE;
-        if (i >= i1) break;
-        load(S[0], j0, page);
-        j0 = clamped(i + 2 * STRIDE);
-        page = page_of(j0);
-        step(S[1]);
-        i += STRIDE;
-        if (i >= i1) break;
+      if (__any(over)) {
+        uint32_t s5 = sm >> 10;
+        uint32_t t = (uint32_t)__shfl_xor((int)s5, 16);
+        s5 = s5 > t ? s5 : t;
+        t = (uint32_t)__shfl_xor((int)s5, 32);
+        s5 = s5 > t ? s5 : t;
+        e5 = __builtin_amdgcn_readfirstlane(e5 > s5 ? e5 : s5);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          const float mm = kv4_over_groups(m[nt], true);
+          if (mm > -__builtin_inff()) top[nt] = fmaxf(top[nt], cf[nt] * mm);
+          const bool seen = top[nt] > -__builtin_inff();
+          const float r = seen ? top[nt] + (float)((int)e5 - 14 - 7) : ref[nt];
+          const float a = seen ? __builtin_amdgcn_exp2f(ref[nt] - r) : 1.0f;
+          ref[nt] = r;
+          l[nt] *= a;
+#pragma unroll
+          for (int k = 0; k < NG; k++) {
+            off[nt][k] *= a;
+            rs[nt][k] *= a;
+          }
+#pragma unroll
+          for (int k = 0; k < VH; k++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) o[nt][k][q] *= a;
+        }
       }
+      // weights (0 for the scores of -inf: cf is not 0), times their value scales
+      uint32_t pf[NT][NG][4];
+      float p[NT][8];
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int t = 0; t < 8; t++) {
+          p[nt][t] = __builtin_amdgcn_exp2f(fmaf(cf[nt], x[nt][t], -ref[nt]));
+          l[nt] += p[nt][t];
+        }
+#pragma unroll
+      for (int k = 0; k < NG; k++)
+#pragma unroll
+        for (int t = 0; t < 8; t += 2) {
+          const uint32_t sa = vs[t >> 2][k][t & 3], sb = vs[t >> 2][k][(t & 3) + 1];
+          const float ma = fmaf(8.0f, kv4_lo(sa), kv4_hi(sa)), mb = fmaf(8.0f, kv4_lo(sb), kv4_hi(sb));
+          const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            const uint32_t w = kv4_pair(p[nt][t] * kv4_lo(sa), p[nt][t + 1] * kv4_lo(sb));
+            pf[nt][k][t >> 1] = w;
+            off[nt][k] = fmaf(p[nt][t + 1], mb, fmaf(p[nt][t], ma, off[nt][k]));
+            rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, w), one, rs[nt][k], false);
+          }
+        }
+      load_scales(j1, page1, true);
+      products();
+      load_codes(j2, page2, false);
+#pragma unroll
+      for (int hh = 0; hh < VH; hh++)
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu;
+          const kv4_u4 a = {(vd[0][2 * hh] >> sh) & m4, (vd[0][2 * hh + 1] >> sh) & m4, (vd[1][2 * hh] >> sh) & m4,
+                            (vd[1][2 * hh + 1] >> sh) & m4};
+          const int grp = (64 * hh + 16 * k) / G;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            const kv4_u4 pb = {pf[nt][grp][0], pf[nt][grp][1], pf[nt][grp][2], pf[nt][grp][3]};
+            o[nt][hh][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(kv4_h8, a),
+                                                                  __builtin_bit_cast(kv4_h8, pb), o[nt][hh][k], 0, 0, 0);
+          }
+        }
+      load_codes(j1, page1, true);
+      scores();
+      load_scales(j2, page2, false);
+      if constexpr (!WIDE) {
+        // products spread between the other operations (64 ragged sequences:
+        // 171 us as the compiler orders them, 160 so; no gain where VALU
+        // operations fill the time)
+#pragma unroll
+        for (int t = 0; t < NT * (2 * KC + 4 * VH); t++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+        }
+      }
+      i += STRIDE;
+      if (i >= i1) break;
+      j0 = j1;
+      j1 = j2;
+      page0 = page1;
+      page1 = page2;
     }
   }
 
@@ -749,63 +767,81 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
         for (int i = 0; i < 4; i++)
           o[nt][hh][k][i] = fmaf(o[nt][hh][k][i], k & 1 ? 1048576.0f : 16777216.0f, off[nt][(64 * hh + 16 * k) / G]);
   }
-  if (!WIDE) {
-    if (wave > 0) {
+  // A value of lane (n, g) is 4 dims of row n: 16 k + 4 g + 0..3.
+  auto put = [&](int nt, int k, kv4_f4 v, float inv) {
+    const uint32_t r = row0 + nt * 16 + n;
+    if (r >= rows) return;
+    const uint32_t t = r / A.ratio, hd = h * A.ratio + (r - t * A.ratio);
+    const uint64_t tok = (uint64_t)(uint32_t)q0 + t;
+    if (used > 1) {
+      *(kv4_f4 *)(A.part_o + ((tok * A.heads + hd) * A.splits + split) * D + 16 * k + 4 * g) = v;
+    } else {
+      const bool bf = A.bf16 != 0;
+      v *= inv;
+      const kv4_u2 w = {(uint32_t)bits_of_f32(v[0], bf) | (uint32_t)bits_of_f32(v[1], bf) << 16,
+                        (uint32_t)bits_of_f32(v[2], bf) | (uint32_t)bits_of_f32(v[3], bf) << 16};
+      *(kv4_u2 *)(A.out + (int64_t)tok * A.o_ts + (int64_t)hd * A.o_hs + 16 * k + 4 * g) = w;
+    }
+  };
+  auto put_weight = [&](int nt, float r0, float w0) {
+    const uint32_t r = row0 + nt * 16 + n;
+    if (g > 0 || r >= rows) return;
+    const uint32_t t = r / A.ratio, hd = h * A.ratio + (r - t * A.ratio);
+    const uint64_t at = ((uint64_t)(uint32_t)q0 + t) * A.heads + hd;
+    if (used > 1) {
+      A.part_ml[(at * A.splits + split) * 2] = r0;
+      A.part_ml[(at * A.splits + split) * 2 + 1] = w0;
+    } else if (A.lse) {
+      A.lse[at] = w0 == 0.0f ? -__builtin_inff() : 0.6931471805599453f * (r0 + __log2f(w0));
+    }
+  };
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const float inv = l[nt] == 0.0f ? 0.0f : 1.0f / l[nt];
+#pragma unroll
+      for (int k = 0; k < VH * 4; k++) put(nt, k, o[nt][k >> 2][k & 3], inv);
+      put_weight(nt, ref[nt], l[nt]);
+    }
+  } else {
+    // every wave joins a quarter of the values, JOIN of a wave at a time in LDS
+    if (g == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) {
-#pragma unroll
-        for (int k = 0; k < VH * 4; k++) join_o[wave - 1][nt * VH * 4 + k][lane] = o[nt][k >> 2][k & 3];
-        if (g == 0) {
-          join_ml[wave - 1][nt][0][n] = ref[nt];
-          join_ml[wave - 1][nt][1][n] = l[nt];
-        }
+        join_ml[wave][nt][0][n] = ref[nt];
+        join_ml[wave][nt][1][n] = l[nt];
       }
     }
-    __syncthreads();
-    if (wave > 0) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++)
+    for (int first = 0; first < VALS; first += JOIN) {
+      if (first) __syncthreads();
 #pragma unroll
-      for (int w = 0; w < 3; w++) {
-        const float r2 = join_ml[w][nt][0][n], l2 = join_ml[w][nt][1][n];
-        // a side without weight counts for nothing, whatever its reference (NaN weights count)
-        const float r = l[nt] == 0.0f ? r2 : l2 == 0.0f ? ref[nt] : fmaxf(ref[nt], r2);
-        const float a = l[nt] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ref[nt] - r);
-        const float b = l2 == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(r2 - r);
-        ref[nt] = r;
-        l[nt] = l[nt] * a + l2 * b;
-#pragma unroll
-        for (int k = 0; k < VH * 4; k++)
-          o[nt][k >> 2][k & 3] = o[nt][k >> 2][k & 3] * a + join_o[w][nt * VH * 4 + k][lane] * b;
+      for (int k = 0; k < JOIN; k++) {
+        const int nt = (first + k) / (VH * 4), kk = (first + k) % (VH * 4);
+        join_o[wave][k][lane] = o[nt][kk >> 2][kk & 3];
       }
-  }
+      __syncthreads();
+      const int nt = first / (VH * 4);               // JOIN values of one tile of rows
+      float a[4], r = -__builtin_inff(), w0 = 0.0f;
+      // a wave without weight counts for nothing, whatever its reference (NaN weights count)
 #pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    const uint32_t r = row0 + nt * 16 + n;
-    if (r >= rows) continue;
-    const uint32_t t = r / A.ratio, hd = h * A.ratio + (r - t * A.ratio);
-    const uint64_t tok = (uint64_t)(uint32_t)q0 + t, at = tok * A.heads + hd;
-    if (used > 1) {
-      float *po = A.part_o + (at * A.splits + split) * D;
+      for (int w = 0; w < 4; w++) r = fmaxf(r, join_ml[w][nt][1][n] == 0.0f ? -1e30f : join_ml[w][nt][0][n]);
 #pragma unroll
-      for (int k = 0; k < VH * 4; k++) *(kv4_f4 *)(po + 16 * k + 4 * g) = o[nt][k >> 2][k & 3];
-      if (g == 0) {
-        A.part_ml[(at * A.splits + split) * 2] = ref[nt];
-        A.part_ml[(at * A.splits + split) * 2 + 1] = l[nt];
+      for (int w = 0; w < 4; w++) {
+        const float lw = join_ml[w][nt][1][n];
+        a[w] = lw == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(join_ml[w][nt][0][n] - r);
+        w0 = fmaf(lw, a[w], w0);
       }
-    } else {
-      const float inv = l[nt] == 0.0f ? 0.0f : 1.0f / l[nt];
-      uint16_t *dst = A.out + (int64_t)tok * A.o_ts + (int64_t)hd * A.o_hs + 4 * g;
+      const float inv = w0 == 0.0f ? 0.0f : 1.0f / w0;
 #pragma unroll
-      for (int k = 0; k < VH * 4; k++) {
-        const kv4_f4 v = o[nt][k >> 2][k & 3];
-        const bool bf = A.bf16 != 0;
-        const kv4_u2 w = {(uint32_t)bits_of_f32(v[0] * inv, bf) | (uint32_t)bits_of_f32(v[1] * inv, bf) << 16,
-                          (uint32_t)bits_of_f32(v[2] * inv, bf) | (uint32_t)bits_of_f32(v[3] * inv, bf) << 16};
-        *(kv4_u2 *)(dst + 16 * k) = w;
+      for (int q = 0; q < JOIN / 4; q++) {
+        const int k = wave * (JOIN / 4) + q;
+        kv4_f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < 4; w++) v += join_o[w][k][lane] * a[w];
+        put(nt, (first + k) % (VH * 4), v, inv);
       }
-      if (A.lse && g == 0)
-        A.lse[at] = l[nt] == 0.0f ? -__builtin_inff() : 0.6931471805599453f * (ref[nt] + __log2f(l[nt]));
+      if (wave == 0 && first % (VH * 4) == 0) put_weight(nt, r, w0);
     }
   }
 }

@@ -24,7 +24,7 @@ lt_status views(const lt_kv4_cache *c, const lt_kv4_batch *b, lt::Kv4View &C, lt
   if (b->n_seqs > 0 && (!b->q_start || !b->kv_len || !b->page_table || b->max_pages == 0)) return LT_ERR_INVALID_ARG;
   if ((((uintptr_t)b->q_start | (uintptr_t)b->kv_len | (uintptr_t)b->page_table) & 3) != 0) return LT_ERR_INVALID_ARG;
   if (!served(c->page_tokens, c->head_dim, c->group)) return LT_ERR_UNSUPPORTED;
-  if (c->n_pages > 0x7FFFFFFFull || c->kv_heads > 65535 || b->n_tokens > 0x7FFFFFFFu || b->n_seqs > 0x7FFFFFFFu)
+  if (c->n_pages > 0x7FFFFFFFull || c->kv_heads > 65535 || b->n_tokens > 0x7FFFFFFFu || b->n_seqs > 65535)
     return LT_ERR_UNSUPPORTED;
   C.pages = c->pages;
   C.n_pages = c->n_pages;
@@ -86,6 +86,27 @@ Plan plan_of(const lt::Kv4View &C, const lt::Kv4Rows &B, uint64_t max_q, uint64_
   return p;
 }
 
+template <int LV>
+void launch_append(dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Rows &B, const lt::Kv4NewRows &N,
+                   uint32_t each) {
+  if (N.bf16) {
+    hipLaunchKernelGGL((lt::kv4_append_kernel<LV, true>), grid, dim3(256), 0, s, C, B, N, each);
+  } else {
+    hipLaunchKernelGGL((lt::kv4_append_kernel<LV, false>), grid, dim3(256), 0, s, C, B, N, each);
+  }
+}
+
+template <int D>
+void launch_read(dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Rows &B, const lt::Kv4ReadRows &R) {
+  if (R.type == LT_F16) {
+    hipLaunchKernelGGL((lt::kv4_read_kernel<D, LT_F16>), grid, dim3(256), 0, s, C, B, R);
+  } else if (R.type == LT_BF16) {
+    hipLaunchKernelGGL((lt::kv4_read_kernel<D, LT_BF16>), grid, dim3(256), 0, s, C, B, R);
+  } else {
+    hipLaunchKernelGGL((lt::kv4_read_kernel<D, LT_F32>), grid, dim3(256), 0, s, C, B, R);
+  }
+}
+
 template <int D, int G, int NT, bool WIDE>
 void launch_rows(dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Rows &B, const lt::Kv4Attn &A) {
   hipLaunchKernelGGL((lt::kv4_attention_kernel<D, G, NT, WIDE>), grid, dim3(256), 0, s, C, B, A);
@@ -101,7 +122,7 @@ void launch_attention(const Plan &p, dim3 grid, hipStream_t s, const lt::Kv4View
     p.nt == 1 ? launch_rows<D, G, 1, false>(grid, s, C, B, A) : launch_rows<D, G, NT, false>(grid, s, C, B, A);
   }
   if (p.splits > 1)
-    hipLaunchKernelGGL((lt::kv4_join_kernel<D>), dim3(B.n_tokens * A.heads), dim3(256), 0, s, C, B, A, p.unit);
+    hipLaunchKernelGGL((lt::kv4_join_kernel<D>), dim3(A.heads, A.max_q, B.n_seqs), dim3(256), 0, s, B, A, p.unit);
 }
 
 }  // namespace
@@ -161,15 +182,20 @@ lt_status lt_kv4_append(const lt_kv4_cache *cache, const lt_kv4_batch *batch, co
   N.neighbours = rows->neighbours != 0;
   N.bf16 = rows->type == LT_BF16;
   N.eps = rows->eps;
-  const uint32_t per = 512 / C.dim;   // tokens a wave takes
-  const uint64_t waves = (uint64_t)((B.n_tokens + per - 1) / per) * (N.heads + 2ull * C.kv_heads);
-  if ((waves + 3) / 4 > 0x7FFFFFFFull) return LT_ERR_UNSUPPORTED;
-  const dim3 grid((uint32_t)((waves + 3) / 4));
+  const uint32_t per = 512 / C.dim, all = N.heads + 2 * C.kv_heads;   // tokens a wave takes, heads of a token
+  const uint32_t chunks = (B.n_tokens + per - 1) / per;
+  // Several heads a wave share what a token costs to look up, and all heads
+  // of a token in one workgroup write its dense row together (8452 tokens of
+  // 48 heads, with reading them back: 95 us with 1 head a wave, 59 with 4, 54
+  // with 12); with few waves each head gets its own.
+  const uint64_t waves = (uint64_t)chunks * all / 8192;
+  const uint32_t each = (uint32_t)(waves < 1 ? 1 : waves > 16 ? 16 : waves);
+  const dim3 grid(chunks, (all + 4 * each - 1) / (4 * each));
   hipStream_t s = (hipStream_t)stream;
   switch (C.dim) {
-    case 64: hipLaunchKernelGGL(lt::kv4_append_kernel<8>, grid, dim3(256), 0, s, C, B, N); break;
-    case 128: hipLaunchKernelGGL(lt::kv4_append_kernel<16>, grid, dim3(256), 0, s, C, B, N); break;
-    default: hipLaunchKernelGGL(lt::kv4_append_kernel<32>, grid, dim3(256), 0, s, C, B, N); break;
+    case 64: launch_append<8>(grid, s, C, B, N, each); break;
+    case 128: launch_append<16>(grid, s, C, B, N, each); break;
+    default: launch_append<32>(grid, s, C, B, N, each); break;
   }
   return launched();
 }
@@ -183,16 +209,20 @@ lt_status lt_kv4_read(const lt_kv4_cache *cache, const lt_kv4_batch *batch, void
   if (type != LT_F16 && type != LT_BF16 && type != LT_F32) return LT_ERR_INVALID_ARG;
   if ((!k && !v) || !aligned16(k) || !aligned16(v) || ((uintptr_t)token_status & 3) != 0) return LT_ERR_INVALID_ARG;
   if (B.n_tokens == 0) return LT_OK;
-  const lt::Kv4ReadRows R{k, v, token_status, (uint32_t)type};
-  const uint32_t per = 512 / C.dim;
-  const uint64_t waves = (uint64_t)((B.n_tokens + per - 1) / per) * 2 * C.kv_heads;
-  if ((waves + 3) / 4 > 0x7FFFFFFFull) return LT_ERR_UNSUPPORTED;
-  const dim3 grid((uint32_t)((waves + 3) / 4));
   hipStream_t s = (hipStream_t)stream;
-  switch (C.dim) {
-    case 64: hipLaunchKernelGGL(lt::kv4_read_kernel<8>, grid, dim3(256), 0, s, C, B, R); break;
-    case 128: hipLaunchKernelGGL(lt::kv4_read_kernel<16>, grid, dim3(256), 0, s, C, B, R); break;
-    default: hipLaunchKernelGGL(lt::kv4_read_kernel<32>, grid, dim3(256), 0, s, C, B, R); break;
+  if (token_status)
+    hipLaunchKernelGGL(lt::kv4_status_kernel, dim3((B.n_tokens + 31) / 32), dim3(256), 0, s, C, B, token_status);
+  if (B.n_seqs > 0) {
+    const lt::Kv4ReadRows R{k, v, (uint32_t)type};
+    // 16-token tiles of the longest sequence; the kernel goes on past them if max_q_len is too low
+    const uint32_t per = C.kv_heads >= 4 ? 4 : C.kv_heads >= 2 ? 2 : 1;
+    const uint64_t tiles = ((uint64_t)batch->max_q_len + 15) / 16 + 1, blocks = (tiles * per + 31) / 32;
+    const dim3 grid((C.kv_heads + per - 1) / per * 8, B.n_seqs, (uint32_t)(blocks < 65535 ? blocks : 65535));
+    switch (C.dim) {
+      case 64: launch_read<64>(grid, s, C, B, R); break;
+      case 128: launch_read<128>(grid, s, C, B, R); break;
+      default: launch_read<256>(grid, s, C, B, R); break;
+    }
   }
   return launched();
 }
@@ -221,7 +251,7 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
   if (!(scale > -3.4e38f && scale < 3.4e38f)) return LT_ERR_INVALID_ARG;
   const Plan p = plan_of(C, B, batch->max_q_len, batch->max_kv_len, heads / C.kv_heads, window, sinks);
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return LT_ERR_INVALID_ARG;
-  if (heads > 65535 || B.n_seqs > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 || (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
+  if (heads > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 || (p.splits > 1 && batch->max_q_len > 65535) || (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
       (uint64_t)batch->max_q_len * (heads / C.kv_heads) > 0x7FFFFFFFull)
     return LT_ERR_UNSUPPORTED;
   if (B.n_tokens == 0 || B.n_seqs == 0 || batch->max_q_len == 0) return LT_OK;

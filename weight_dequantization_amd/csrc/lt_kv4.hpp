@@ -77,8 +77,7 @@ struct Kv4NewRows {
   float eps;
 };
 
-__device__ __forceinline__ void load8(const uint16_t *p, bool bf16, float v[8]) {
-  const uint4 d = *(const uint4 *)p;
+__device__ __forceinline__ void unpack8(uint4 d, bool bf16, float v[8]) {
   const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
   for (int i = 0; i < 8; i++) v[i] = f32_of_bits((uint16_t)(w[i >> 1] >> (16 * (i & 1))), bf16);
@@ -93,212 +92,342 @@ __device__ __forceinline__ void store8(uint16_t *p, bool bf16, const float v[8])
 }
 
 // One head vector per LV = dim / 8 lanes, 8 neighbouring values a lane; a
-// wave takes 64 / LV consecutive tokens of one head, so its K rows, its V
-// units (4 tokens side by side) and its loads each fall together.  The
-// rotation's products and sums are rounded one by one (no contraction), as
-// its formula reads.
-template <int LV>
-__global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View C, Kv4Rows B, Kv4NewRows N) {
-  constexpr uint32_t TPW = 64 / LV;
+// wave takes 64 / LV consecutive tokens, so that its K rows, its V units (4
+// tokens side by side) and its loads each fall together, and `heads_each`
+// heads of theirs one after another, for which a token's place and rotation
+// are fetched once.  The rotation's products and sums are rounded one by one
+// (no contraction), as its formula reads.
+template <int LV, bool BF16>
+__global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View C, Kv4Rows B, Kv4NewRows N, uint32_t heads_each) {
+  constexpr uint32_t TPW = 64 / LV, D = 8 * LV;
   const uint32_t lane = threadIdx.x & 63u, j = lane % LV;
   const uint32_t all = N.heads + 2 * C.kv_heads;
-  const uint64_t w = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const uint32_t hd = (uint32_t)(w % all);
-  const uint64_t t64 = w / all * TPW + lane / LV;
+  const uint32_t first = (blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * heads_each;
+  const uint64_t t64 = (uint64_t)blockIdx.x * TPW + lane / LV;
   const uint32_t t = t64 < B.n_tokens ? (uint32_t)t64 : B.n_tokens;   // n_tokens: no row
-  const bool bf16 = N.bf16 != 0;
-  Kv4Token k = kv4_token<LV>(C, B, t, j);
+  if (first >= all) return;
+  const Kv4Token k = kv4_token<LV>(C, B, t, j);
   const bool live = k.seq >= 0;
   int32_t row = k.pos;
   if (live && N.positions) row = N.positions[t];
   const bool turned = N.cos != nullptr;
   const bool bad = k.page < 0 || (turned && (row < 0 || (uint32_t)row >= N.rope_len));
-  if (!live || bad) row = 0;
-
-  const bool is_q = hd < N.heads, is_v = hd >= N.heads + C.kv_heads;
-  const uint32_t h = is_q ? hd : is_v ? hd - N.heads - C.kv_heads : hd - N.heads;
-  float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (live) {
-    const uint16_t *src = is_q ? N.q + (int64_t)t * N.q_ts + (int64_t)h * N.q_hs
-                               : is_v ? N.v + (int64_t)t * N.v_ts + (int64_t)h * N.v_hs
-                                      : N.k + (int64_t)t * N.k_ts + (int64_t)h * N.k_hs;
-    load8(src + 8 * j, bf16, y);
-  }
-  if (N.status && hd == N.heads && j == 0 && t < B.n_tokens)
+  if (N.status && first <= N.heads && N.heads < first + heads_each && j == 0 && t < B.n_tokens)
     N.status[t] = live && bad ? LT_CHUNK_BAD_TABLE : LT_CHUNK_OK;
+  const bool put = live && !bad;
+  if (!put) row = 0;
 
-  if (!is_v) {
-    const uint16_t *wt = is_q ? N.q_norm : N.k_norm;
-    if (wt) {
-      float ss = 0.0f, wv[8];
+  // the token's rotation: for pairs half a rotary dim apart, the angles of
+  // this lane's 8 values; for neighbours, of its 4 pairs
+  const uint32_t half = N.rotary / 2;
+  const bool in = 8 * j < N.rotary, second = 8 * j >= half;
+  float cs[8], sn[8];
+  if (turned && in) {
+    const uint32_t i0 = N.neighbours ? 4 * j : second ? 8 * j - half : 8 * j;
+    const float *cr = N.cos + (uint64_t)row * half + i0, *sr = N.sin + (uint64_t)row * half + i0;
+    auto four = [&](int q) {
+      const float4 c = ((const float4 *)cr)[q], s = ((const float4 *)sr)[q];
+      cs[4 * q] = c.x, cs[4 * q + 1] = c.y, cs[4 * q + 2] = c.z, cs[4 * q + 3] = c.w;
+      sn[4 * q] = s.x, sn[4 * q + 1] = s.y, sn[4 * q + 2] = s.z, sn[4 * q + 3] = s.w;
+    };
+    four(0);
+    if (!N.neighbours) four(1);
+  }
+  const uint32_t slot = (uint32_t)k.pos & ((1u << C.page_shift) - 1), lg = C.group / 8;
+  const uint32_t last = first + heads_each < all ? first + heads_each : all;
+
+  // the next head's values are on their way while one is worked on
+  auto fetch = [&](uint32_t hd) {
+    const uint16_t *src;
+    if (hd < N.heads)
+      src = N.q + (int64_t)t * N.q_ts + (int64_t)hd * N.q_hs;
+    else if (hd < N.heads + C.kv_heads)
+      src = N.k + (int64_t)t * N.k_ts + (int64_t)(hd - N.heads) * N.k_hs;
+    else
+      src = N.v + (int64_t)t * N.v_ts + (int64_t)(hd - N.heads - C.kv_heads) * N.v_hs;
+    return live ? *(const uint4 *)(src + 8 * j) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 next = fetch(first), wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (N.q_norm) wq = *(const uint4 *)(N.q_norm + 8 * j);
+  if (N.k_norm) wk = *(const uint4 *)(N.k_norm + 8 * j);
+  for (uint32_t hd = first; hd < last; hd++) {
+    const bool is_q = hd < N.heads, is_v = hd >= N.heads + C.kv_heads;
+    const uint32_t h = is_q ? hd : is_v ? hd - N.heads - C.kv_heads : hd - N.heads;
+    float y[8];
+    unpack8(next, BF16, y);
+    if (hd + 1 < last) next = fetch(hd + 1);
+    if (!is_v) {
+      if ((is_q ? N.q_norm : N.k_norm) != nullptr) {
+        float ss = 0.0f, wv[8];
 #pragma unroll
-      for (int i = 0; i < 8; i++) ss = fmaf(y[i], y[i], ss);
+        for (int i = 0; i < 8; i++) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
-      for (int d = 1; d < LV; d <<= 1) ss += __shfl_xor(ss, d);
-      const float inv = rsqrtf(ss / (float)C.dim + N.eps);
-      load8(wt + 8 * j, bf16, wv);
+        for (int d = 1; d < LV; d <<= 1) ss += __shfl_xor(ss, d);
+        const float inv = rsqrtf(ss * (1.0f / D) + N.eps);
+        unpack8(is_q ? wq : wk, BF16, wv);
 #pragma unroll
-      for (int i = 0; i < 8; i++) y[i] = y[i] * inv * wv[i];
-    }
-    if (turned) {
-      const uint32_t half = N.rotary / 2;
-      const float *cr = N.cos + (uint64_t)row * half, *sr = N.sin + (uint64_t)row * half;
-      if (N.neighbours) {
-        if (8 * j < N.rotary) {
-          const float4 c = *(const float4 *)(cr + 4 * j), s = *(const float4 *)(sr + 4 * j);
-          const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+        for (int i = 0; i < 8; i++) y[i] = y[i] * inv * wv[i];
+      }
+      if (turned && N.neighbours) {
+        if (in) {
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const float a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
-            y[2 * i + 1] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
+            y[2 * i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
+            y[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
           }
         }
-      } else {
+      } else if (turned) {
         // the other value of each pair is rotary / 16 lanes away
-        const bool second = 8 * j >= half, in = 8 * j < N.rotary;
-        const uint32_t i0 = second ? 8 * j - half : 8 * j;
-        const int other = (int)lane + (in ? (second ? -(int)(half / 8) : (int)(half / 8)) : 0);
         float o[8];
+        if (LV == 16 && N.rotary == D) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) o[i] = __shfl(y[i], other);
+          for (int i = 0; i < 8; i++)   // 8 lanes on within 16
+            o[i] = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y[i]), 0x128, 0xF, 0xF, true));
+        } else {
+          const int other = (int)lane + (in ? (second ? -(int)(half / 8) : (int)(half / 8)) : 0);
+#pragma unroll
+          for (int i = 0; i < 8; i++) o[i] = __shfl(y[i], other);
+        }
         if (in) {
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            const float c = cr[i0 + i], s = sr[i0 + i];
-            y[i] = second ? __fadd_rn(__fmul_rn(y[i], c), __fmul_rn(o[i], s))
-                          : __fsub_rn(__fmul_rn(y[i], c), __fmul_rn(o[i], s));
+            const float a = __fmul_rn(y[i], cs[i]), b = __fmul_rn(o[i], sn[i]);
+            y[i] = __fadd_rn(a, second ? b : -b);
           }
         }
       }
     }
-  }
-  if (is_q) {
-    if (live) {
-      if (bad) {
+    if (is_q) {
+      if (live) {
+        if (bad) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) y[i] = __builtin_nanf("");
+          for (int i = 0; i < 8; i++) y[i] = __builtin_nanf("");
+        }
+        store8(N.q_out + (int64_t)t * N.o_ts + (int64_t)h * N.o_hs + 8 * j, BF16, y);
       }
-      store8(N.q_out + (int64_t)t * N.o_ts + (int64_t)h * N.o_hs + 8 * j, bf16, y);
+      continue;
     }
-    return;
-  }
 
-  // the group's range, over group / 8 lanes
-  const uint32_t lg = C.group / 8;
-  bool odd = false;
-  float lo = __builtin_inff(), hi = -__builtin_inff();
+    // the group's range, over group / 8 lanes; 0 times a value that is not finite is NaN
+    float lo = y[0], hi = y[0], odd = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    odd |= !(fabsf(y[i]) <= 3.402823466e38f);
-    y[i] = fminf(fmaxf(y[i], -65504.0f), 65504.0f);
-    lo = fminf(lo, y[i]);
-    hi = fmaxf(hi, y[i]);
-  }
-  uint32_t oddv = odd;
-  for (uint32_t d = 1; d < lg; d <<= 1) {
-    lo = fminf(lo, __shfl_xor(lo, (int)d));
-    hi = fmaxf(hi, __shfl_xor(hi, (int)d));
-    oddv |= __shfl_xor(oddv, (int)d);
-  }
-  uint16_t mb = f16_of_f32(lo), sb = f16_of_f32((hi - lo) / 15.0f);
-  const float m = f32_of_f16(mb), s = f32_of_f16(sb);
-  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-  uint32_t codes = 0;
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float c = fminf(fmaxf(rintf((y[i] - m) * inv), 0.0f), 15.0f);
-    codes |= (uint32_t)c << (4 * i);
-  }
-  if (oddv) {
-    codes = 0;
-    sb = 0;
-    mb = 0x7E00u;
-  }
-  const bool put = live && !bad;
-  const uint32_t slot = (uint32_t)k.pos & ((1u << C.page_shift) - 1);
-  uint8_t *blk = put ? kv4_block(C, (uint32_t)k.page, h) : nullptr;
-  if (is_v) {
-    // values 16 apart share a unit: the 4 lanes that hold them exchange
-    // their codes, and lane n of them writes units 8 b + 2 n and + 1
-    const uint32_t jj = j & 7, b = jj & 1, n = jj >> 1;
-    uint32_t d[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) d[i] = __shfl(codes, (int)((lane & ~7u) + 2 * i + b));
-    if (put) {
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const uint32_t sh = 4 * (2 * n + e);
-        uint32_t u = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++) u |= ((d[i] >> sh) & 15u) << (4 * i);
-        *(uint16_t *)(blk + C.kc + C.sc + kv4_v_unit(C, slot, 8 * b + 2 * n + e, j >> 3)) = (uint16_t)u;
-      }
+    for (int i = 0; i < 8; i++) {
+      lo = fminf(lo, y[i]);
+      hi = fmaxf(hi, y[i]);
+      odd = fmaf(y[i], 0.0f, odd);
     }
-    blk += C.kc + C.sc + C.kc;
-  } else {
-    if (put) *(uint32_t *)(blk + kv4_k_row(C, slot) + 4 * ((j & 3) * (C.dim / 32) + (j >> 2))) = codes;
-    blk += C.kc;
+    for (uint32_t d = 1; d < lg; d <<= 1) {
+      lo = fminf(lo, __shfl_xor(lo, (int)d));
+      hi = fmaxf(hi, __shfl_xor(hi, (int)d));
+      odd += __shfl_xor(odd, (int)d);
+    }
+    lo = fminf(fmaxf(lo, -65504.0f), 65504.0f);      // values past them get codes 0 and 15
+    hi = fminf(fmaxf(hi, -65504.0f), 65504.0f);
+    uint16_t mb = f16_of_f32(lo), sb = f16_of_f32((hi - lo) / 15.0f);
+    const float m = f32_of_f16(mb), s = f32_of_f16(sb);
+    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    uint32_t even = 0, odds = 0;                     // codes 0, 2, 4, 6 and 1, 3, 5, 7 in bytes
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float c0 = fminf(fmaxf(rintf((y[i] - m) * inv), 0.0f), 15.0f);
+      const float c1 = fminf(fmaxf(rintf((y[i + 1] - m) * inv), 0.0f), 15.0f);
+      even = __builtin_amdgcn_cvt_pk_u8_f32(c0, i / 2, even);
+      odds = __builtin_amdgcn_cvt_pk_u8_f32(c1, i / 2, odds);
+    }
+    uint32_t codes = even | odds << 4;
+    if (odd != 0.0f) {                               // NaN
+      codes = 0;
+      sb = 0;
+      mb = 0x7E00u;
+    }
+    uint8_t *blk = put ? kv4_block(C, (uint32_t)k.page, h) : nullptr;
+    if (is_v) {
+      // values 16 apart share a unit: the 4 lanes that hold them exchange
+      // their codes, and lane n of them writes units 8 b + 2 n and + 1
+      const uint32_t jj = j & 7, b = jj & 1, n = jj >> 1;
+      uint32_t d[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) d[i] = __shfl(codes, (int)((lane & ~7u) + 2 * i + b));
+      if (put) {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const uint32_t sh = 4 * (2 * n + e);
+          uint32_t u = 0;
+#pragma unroll
+          for (int i = 0; i < 4; i++) u |= ((d[i] >> sh) & 15u) << (4 * i);
+          *(uint16_t *)(blk + C.kc + C.sc + kv4_v_unit(C, slot, 8 * b + 2 * n + e, j >> 3)) = (uint16_t)u;
+        }
+      }
+      blk += C.kc + C.sc + C.kc;
+    } else {
+      if (put) *(uint32_t *)(blk + kv4_k_row(C, slot) + 4 * ((j & 3) * (D / 32) + (j >> 2))) = codes;
+      blk += C.kc;
+    }
+    if (put && j % lg == 0) *(uint32_t *)(blk + kv4_scale(C, slot, j / lg)) = (uint32_t)sb | ((uint32_t)mb << 16);
   }
-  if (put && j % lg == 0) *(uint32_t *)(blk + kv4_scale(C, slot, j / lg)) = (uint32_t)sb | ((uint32_t)mb << 16);
 }
 
 // -------------------------------------------------------------------- read
 
 struct Kv4ReadRows {
   void *k, *v;
-  int32_t *status;
   uint32_t type;
 };
 
-// As the append: LV lanes a head vector, 8 values a lane.
-template <int LV>
-__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4View C, Kv4Rows B, Kv4ReadRows R) {
-  constexpr uint32_t TPW = 64 / LV;
-  const uint32_t lane = threadIdx.x & 63u, j = lane % LV;
-  const uint32_t all = 2 * C.kv_heads;
-  const uint64_t w = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const uint32_t hd = (uint32_t)(w % all);
-  const uint64_t t64 = w / all * TPW + lane / LV;
-  const uint32_t t = t64 < B.n_tokens ? (uint32_t)t64 : B.n_tokens;
-  const Kv4Token k = kv4_token<LV>(C, B, t, j);
-  const bool live = k.seq >= 0, is_v = hd >= C.kv_heads;
-  const uint32_t h = is_v ? hd - C.kv_heads : hd;
-  if (R.status && hd == 0 && j == 0 && t < B.n_tokens)
-    R.status[t] = live && k.page < 0 ? LT_CHUNK_BAD_TABLE : LT_CHUNK_OK;
-  void *out = is_v ? R.v : R.k;
-  if (!live || !out) return;
-  float y[8];
-  if (k.page < 0) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) y[i] = __builtin_nanf("");
-  } else {
-    const uint32_t slot = (uint32_t)k.pos & ((1u << C.page_shift) - 1);
-    const uint8_t *blk = kv4_block(C, (uint32_t)k.page, h);
-    uint32_t codes = 0;
-    if (is_v) {
-      blk += C.kc + C.sc;
-      const uint32_t jj = j & 7, n = jj >> 1;
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const uint32_t u = *(const uint16_t *)(blk + kv4_v_unit(C, slot, 8 * (jj & 1) + e, j >> 3));
-        codes |= ((u >> (4 * n)) & 15u) << (4 * e);
-      }
+__global__ void __launch_bounds__(256) kv4_status_kernel(Kv4View C, Kv4Rows B, int32_t *status) {
+  const uint32_t lane = threadIdx.x & 63u, t = blockIdx.x * 32 + threadIdx.x / 8;
+  const Kv4Token k = kv4_token<8>(C, B, t, lane & 7u);
+  if ((lane & 7u) == 0 && t < B.n_tokens) status[t] = k.seq >= 0 && k.page < 0 ? LT_CHUNK_BAD_TABLE : LT_CHUNK_OK;
+}
+
+// Pairs of codes (in the low bits of both halves) to s c + m in the wanted
+// type: fp16 by one packed multiply-add (1024 + c is fp16 with c in its last
+// bits), the others by one in fp32; either rounds once.
+template <int TYPE>
+struct Kv4Out {
+  float s, m;
+  uint32_t w[TYPE == LT_F32 ? 8 : 4];
+  __device__ __forceinline__ void two(int i, uint32_t c) {   // values 2 i, 2 i + 1
+    typedef _Float16 h2v __attribute__((ext_vector_type(2)));
+    if constexpr (TYPE == LT_F16) {
+      const h2v base = {(_Float16)1024.0f, (_Float16)1024.0f}, s2 = {(_Float16)s, (_Float16)s}, m2 = {(_Float16)m, (_Float16)m};
+      const h2v q = __builtin_bit_cast(h2v, c | 0x64006400u) - base;
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(q, s2, m2));
     } else {
-      codes = *(const uint32_t *)(blk + kv4_k_row(C, slot) + 4 * ((j & 3) * (C.dim / 32) + (j >> 2)));
+      const float a = fmaf((float)(c & 0xFFu), s, m), b = fmaf((float)((c >> 16) & 0xFFu), s, m);
+      if constexpr (TYPE == LT_F32) {
+        w[2 * i] = __builtin_bit_cast(uint32_t, a);
+        w[2 * i + 1] = __builtin_bit_cast(uint32_t, b);
+      } else {
+        w[i] = (uint32_t)bf16_of_f32(a) | (uint32_t)bf16_of_f32(b) << 16;
+      }
     }
-    const uint32_t sm = *(const uint32_t *)(blk + C.kc + kv4_scale(C, slot, j / (C.group / 8)));
-    const float s = f32_of_f16((uint16_t)sm), m = f32_of_f16((uint16_t)(sm >> 16));
-#pragma unroll
-    for (int i = 0; i < 8; i++) y[i] = fmaf((float)((codes >> (4 * i)) & 15u), s, m);
   }
-  const uint64_t at = ((uint64_t)t * C.kv_heads + h) * C.dim + 8 * j;
-  if (R.type == LT_F32) {
-    float4 *o = (float4 *)((float *)out + at);
-    o[0] = make_float4(y[0], y[1], y[2], y[3]);
-    o[1] = make_float4(y[4], y[5], y[6], y[7]);
-  } else {
-    store8((uint16_t *)out + at, R.type == LT_BF16, y);
+  __device__ __forceinline__ void store(void *p, uint64_t at) const {   // 8 values from element `at` on
+    if constexpr (TYPE == LT_F32) {
+      *(uint4 *)((float *)p + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      *(uint4 *)((float *)p + at + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      *(uint4 *)((uint16_t *)p + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+};
+
+// Four neighbouring lanes hold 4 dwords each: dword k of lane i goes to dword
+// i of lane k.
+__device__ __forceinline__ void kv4_turn(uint32_t (&w)[4], uint32_t lane) {
+  auto swap = [&](uint32_t &a, uint32_t &b, bool up, auto other) {   // a of the upper lane with b of the lower
+    const uint32_t t = other(up ? a : b);
+    a = up ? t : a;
+    b = up ? b : t;
+  };
+  auto x1 = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true); };
+  auto x2 = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true); };
+  swap(w[0], w[1], lane & 1u, x1);
+  swap(w[2], w[3], lane & 1u, x1);
+  swap(w[0], w[2], lane & 2u, x2);
+  swap(w[1], w[3], lane & 2u, x2);
+}
+
+// A wave takes 16 tokens that lie together in a page, of one head, and writes
+// runs of 64 bytes and more: K rows by lane (token, quarter); V units by lane
+// (64 values, 8 of the 16 units, token), where the 4 lanes of 4 tokens
+// exchange their codes so that each has one run of 16 values of all 4.
+template <int D, int TYPE>
+__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4View C, Kv4Rows B, Kv4ReadRows R) {
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  // A dense row of all heads is often a multiple of 2 KiB, so the same head of
+  // different tokens falls into few channels of an L2.  Workgroups go to the
+  // 8 L2s in turn: block x takes tile x % 8 of 8 and a group of up to 4 heads,
+  // so that all heads of a token are written from one L2 at about one time
+  // (XXX us with a head an L2, XXX so, for 16 prefixes).
+  const uint32_t per = C.kv_heads >= 4 ? 4 : C.kv_heads >= 2 ? 2 : 1;   // heads of a workgroup
+  const uint32_t h = (blockIdx.x >> 3) * per + wave % per, seq = blockIdx.y;
+  if (h >= C.kv_heads) return;
+  const int32_t q0 = B.q_start[seq], q1 = B.q_start[seq + 1], kvl = B.kv_len[seq];
+  if (q0 < 0 || q1 <= q0 || (uint32_t)q1 > B.n_tokens || kvl <= 0) return;
+  const int32_t p0 = kvl - (q1 - q0);                // position of row q0
+  const uint32_t t0 = p0 > 0 ? (uint32_t)p0 / 16 : 0, t1 = ((uint32_t)kvl + 15) / 16, at_once = 4 / per;
+  for (uint32_t tile = t0 + (blockIdx.z * 8 + (blockIdx.x & 7u)) * at_once + wave / per; tile < t1;
+       tile += gridDim.z * 8 * at_once) {
+    const uint32_t pi = (16 * tile) >> C.page_shift, slot = (16 * tile) & ((1u << C.page_shift) - 1);
+    const int32_t page = pi < B.max_pages ? B.table[(uint64_t)seq * B.max_pages + pi] : -1;
+    const bool bad = page < 0 || (uint64_t)page >= C.n_pages;
+    const uint8_t *blk = kv4_block(C, bad ? 0u : (uint32_t)page, h);
+    // everything the tile needs is loaded before anything is stored
+    const uint32_t n = lane >> 2, g = lane & 3u;     // K: token and quarter
+    // V: 4 tokens' units and 64 values' lie side by side: lanes i, b, h, g
+    constexpr uint32_t VH = D / 64, W = VH < 2 ? 1 : 2, RUNS = VH / W;
+    const uint32_t i = lane & 3u, b = (lane >> 2) & 1u, hh = (lane >> 3) % W, gg = ((lane >> 3) / W) & 3u;
+    const bool spare = (lane >> 3) / W > 3;          // 64 values: half the lanes cover the units
+    uint32_t d[D / 32], ks[D / 32], u[RUNS][4], vs[RUNS][4];
+    const uint8_t *vblk = blk + C.kc + C.sc;
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2) {
+      const uint2 two = *(const uint2 *)(blk + kv4_k_row(C, slot + n) + g * (D / 8) + 4 * c);
+      d[c] = two.x;
+      d[c + 1] = two.y;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; c++) ks[c] = *(const uint32_t *)(blk + C.kc + kv4_scale(C, slot + n, 32 * c / C.group));
+#pragma unroll
+    for (int r = 0; r < (int)RUNS; r++) {
+      const uint32_t hv = r * W + hh;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const uint8_t *src = vblk + kv4_v_unit(C, slot + 4 * gg + i, 8 * b + 2 * e, hv);
+        u[r][e] = (uint32_t)*(const uint16_t *)src | (uint32_t)*(const uint16_t *)(src + D / 8) << 16;
+      }
+      // the scales of 4 tokens: 16 bytes
+      const uint4 four = *(const uint4 *)(vblk + C.kc + kv4_scale(C, slot + 4 * gg, (64 * hv + 16 * i) / C.group));
+      vs[r][0] = four.x, vs[r][1] = four.y, vs[r][2] = four.z, vs[r][3] = four.w;
+    }
+    auto with = [&](uint32_t sm) {
+      Kv4Out<TYPE> o;
+      sm = bad ? 0x7E000000u : sm;
+      o.s = f32_of_f16((uint16_t)sm);
+      o.m = f32_of_f16((uint16_t)(sm >> 16));
+      return o;
+    };
+    if (R.k) {
+      const int32_t p = (int32_t)(16 * tile + n);
+      const uint64_t at = ((uint64_t)(uint32_t)(q0 + p - p0) * C.kv_heads + h) * D + 8 * g;
+#pragma unroll
+      for (int c = 0; c < D / 32; c++) {
+        Kv4Out<TYPE> o = with(ks[c]);
+        // neighbouring codes of a byte to the halves of a dword
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const uint32_t two = d[c] >> (8 * e);
+          o.two(e, (two & 15u) | (two & 0xF0u) << 12);
+        }
+        if (p >= p0 && p < kvl) o.store(R.k, at + 32 * c);
+      }
+    }
+    if (R.v) {
+#pragma unroll
+      for (int r = 0; r < (int)RUNS; r++) {
+        // run k of the token: unit 2 e in nibble e, unit 2 e + 1 in nibble e + 4
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          w[k] = 0;
+#pragma unroll
+          for (int e = 0; e < 4; e++) w[k] |= ((u[r][e] >> (4 * k)) & 0x000F000Fu) << (4 * e);
+        }
+        kv4_turn(w, lane);                           // now dword k: run i of token k
+        const uint32_t d0 = 64 * (r * W + hh) + 16 * i + 8 * b;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const int32_t p = (int32_t)(16 * tile + 4 * gg + k);
+          Kv4Out<TYPE> o = with(vs[r][k]);
+#pragma unroll
+          for (int e = 0; e < 4; e++) o.two(e, (w[k] >> (4 * e)) & 0x000F000Fu);
+          if (p >= p0 && p < kvl && !spare) o.store(R.v, ((uint64_t)(uint32_t)(q0 + p - p0) * C.kv_heads + h) * D + d0);
+        }
+      }
+    }
   }
 }
 
@@ -846,31 +975,28 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   }
 }
 
-// Joins the splits of a row: one workgroup a row, D / 4 threads a split.
+// Joins the splits of a row: one workgroup a row (head, token of its sequence,
+// sequence), D / 4 threads a split, 4 splits' loads at a time.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_join_kernel(Kv4View C, Kv4Rows B, Kv4Attn A, uint32_t unit) {
+__global__ void __launch_bounds__(256) kv4_join_kernel(Kv4Rows B, Kv4Attn A, uint32_t unit) {
   constexpr uint32_t T = D / 4, S = 256 / T;
   __shared__ kv4_f4 sum_o[S][T];
   __shared__ float sum_ml[S][2];
-  const uint32_t t = blockIdx.x / A.heads, hd = blockIdx.x % A.heads;
+  const uint32_t hd = blockIdx.x, tok = blockIdx.y, seq = blockIdx.z;
   const uint32_t d = threadIdx.x % T, s0 = threadIdx.x / T;
-  uint32_t cnt = 0;
-  for (uint32_t b = threadIdx.x & 63u; b < B.n_seqs; b += 64) cnt += (uint32_t)(B.q_start[b + 1] <= (int32_t)t);
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) cnt += __shfl_xor(cnt, k);
-  if (cnt >= B.n_seqs) return;
-  const int32_t q0 = B.q_start[cnt], q1 = B.q_start[cnt + 1];
-  const int32_t kvl = B.kv_len[cnt] > 0 ? B.kv_len[cnt] : 0;
-  if (q0 < 0 || (int32_t)t < q0 || (uint32_t)q1 > B.n_tokens || t - (uint32_t)q0 >= A.max_q) return;
+  const int32_t q0 = B.q_start[seq], q1 = B.q_start[seq + 1];
+  const int32_t kvl = B.kv_len[seq] > 0 ? B.kv_len[seq] : 0;
+  if (q0 < 0 || q1 <= q0 || (uint32_t)q1 > B.n_tokens || tok >= (uint32_t)(q1 - q0)) return;
   // the tiles of the rows that were taken together with this one
   const uint32_t nq = (uint32_t)(q1 - q0) < A.max_q ? (uint32_t)(q1 - q0) : A.max_q, rows = nq * A.ratio;
-  const uint32_t row0 = ((t - (uint32_t)q0) * A.ratio + hd % A.ratio) / unit * unit;
+  const uint32_t row0 = (tok * A.ratio + hd % A.ratio) / unit * unit;
   const uint32_t row1 = row0 + unit < rows ? row0 + unit : rows;
   const int32_t p_base = kvl - (q1 - q0);
   const Kv4Tiles tiles = kv4_tiles(p_base + (int32_t)(row0 / A.ratio), p_base + (int32_t)((row1 - 1) / A.ratio), A.window,
                                    A.sinks);
   const uint32_t used = kv4_used(tiles.total, A);
   if (used <= 1) return;
+  const uint32_t t = (uint32_t)q0 + tok;
   const uint64_t at = (uint64_t)t * A.heads + hd;
   const float *ml = A.part_ml + at * A.splits * 2, *po = A.part_o + at * A.splits * D + 4 * d;
   float ref = 0.0f, l = 0.0f;
@@ -883,7 +1009,20 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4View C, Kv4Rows B, Kv4
     l = l * a + l2 * b;
     o = o * a + o2 * b;
   };
-  for (uint32_t s = s0; s < used; s += S) add(ml[2 * s], ml[2 * s + 1], *(const kv4_f4 *)(po + (uint64_t)s * D));
+  for (uint32_t s = s0; s < used; s += 4 * S) {
+    float r2[4], l2[4];
+    kv4_f4 o2[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++) {
+      const uint32_t sk = s + k * S < used ? s + k * S : s;
+      r2[k] = ml[2 * sk];
+      l2[k] = ml[2 * sk + 1];
+      o2[k] = *(const kv4_f4 *)(po + (uint64_t)sk * D);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++)
+      if (s + k * S < used) add(r2[k], l2[k], o2[k]);
+  }
   sum_o[s0][d] = o;
   if (d == 0) {
     sum_ml[s0][0] = ref;

@@ -80,7 +80,8 @@ Plan plan_of(const lt::Kv4View &C, const lt::Kv4Rows &B, uint64_t max_q, uint64_
     chunk = chunk < 16 ? 16 : chunk > 128 ? 128 : chunk;
   }
   p.chunk_shift = 0;
-  while ((1ull << p.chunk_shift) < chunk) p.chunk_shift++;
+  // a power of two: all tiles where they are not split, the one near `chunk` else
+  while (chunk < tiles ? 3 * (1ull << p.chunk_shift) < chunk * 2 : (1ull << p.chunk_shift) < tiles) p.chunk_shift++;
   p.splits = (uint32_t)((tiles + (1ull << p.chunk_shift) - 1) >> p.chunk_shift);
   p.bytes = p.splits > 1 ? (uint64_t)B.n_tokens * C.kv_heads * ratio * p.splits * (C.dim + 2) * 4 : 0;
   return p;
@@ -251,7 +252,8 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
   if (!(scale > -3.4e38f && scale < 3.4e38f)) return LT_ERR_INVALID_ARG;
   const Plan p = plan_of(C, B, batch->max_q_len, batch->max_kv_len, heads / C.kv_heads, window, sinks);
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return LT_ERR_INVALID_ARG;
-  if (heads > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 || (p.splits > 1 && batch->max_q_len > 65535) || (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
+  if (heads > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 || (p.splits > 1 && batch->max_q_len > 65535) ||
+      (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
       (uint64_t)batch->max_q_len * (heads / C.kv_heads) > 0x7FFFFFFFull)
     return LT_ERR_UNSUPPORTED;
   if (B.n_tokens == 0 || B.n_seqs == 0 || batch->max_q_len == 0) return LT_OK;

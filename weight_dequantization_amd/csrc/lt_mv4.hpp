@@ -164,13 +164,6 @@ __device__ __forceinline__ f4 mv4_mfma(uint4 a, uint4 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
 
-// Orders this wave's LDS accesses by different lanes (the hardware keeps the
-// order of one wave's operations; this keeps the compiler's).
-__device__ __forceinline__ void mv4_wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Four lanes 16 apart hold 4 dwords each: dword k of lane group g goes to
 // dword g of lane group k.
 __device__ __forceinline__ void mv4_transpose(uint32_t d[4]) {
@@ -284,7 +277,7 @@ __global__ void __launch_bounds__(64 * NW) mv4_kernel(Mv4Params P) {
   };
   if (wave < nblk) fetch(wave);
   for (uint32_t blk = wave; blk < nblk; blk += NW) {
-    mv4_wave_order();   // after the last block's reads
+    wave_order();   // after the last block's reads
 #pragma unroll
     for (int i = 0; i < WI; i++) {
       const uint32_t r = i * (64 / CW) + lane / CW;
@@ -295,7 +288,7 @@ __global__ void __launch_bounds__(64 * NW) mv4_kernel(Mv4Params P) {
       const uint32_t b = i * (64 / CX) + lane / CX;
       if (b < XR) *(uint4 *)(xl + b * (16 * CX) + 16 * ((lane % CX) ^ (b & 7u))) = mv4_vector(xd[i]);
     }
-    mv4_wave_order();
+    wave_order();
     uint32_t sc[(GPI + 1) / 2], zc[(GPI + 3) / 4];
 #pragma unroll
     for (int k = 0; k < (GPI + 1) / 2; k++) sc[k] = sd[k];

@@ -1,5 +1,6 @@
 // lt_types.hpp -- 16-bit element types on the device: fp16 and bf16 bits to
-// fp32 (exact) and back (round to nearest even).
+// fp32 (exact) and back (round to nearest even); the order of a wave's LDS
+// accesses.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -23,6 +24,13 @@ __device__ __forceinline__ void store_as(void *p, uint64_t i, float v, uint32_t 
   } else {
     ((uint16_t *)p)[i] = bits_of_f32(v, type == LT_BF16);
   }
+}
+
+// Orders this wave's LDS accesses by different lanes (the hardware keeps the
+// order of one wave's operations; this keeps the compiler's).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 }  // namespace lt

@@ -35,29 +35,34 @@ bool launch_tiles(const lt::Mv4Params &P, hipStream_t s) {
   if (lds > 65536 &&
       hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return false;
-  hipLaunchKernelGGL(kernel, dim3((P.rows + 16 * RT - 1) / (16 * RT)), dim3(64 * NW), lds, s, P);
+  const uint32_t blocks = ((P.rows + 16 * RT - 1) / (16 * RT) + 7) / 8 * 8 * ((P.batch + XR - 1) / XR);
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * NW), lds, s, P);
   return true;
 }
 
-// The workgroup's shape by the number of vectors.  Two tiles of rows a
-// workgroup halve what x costs (40 us against 51 at 8192 x 28672, 16
-// vectors); with fewer rows than fill the CUs that way, one.  Blocks of 256
-// columns give whole 128-byte lines of W (34 us against 40, 8 vectors); with
-// small groups the registers of their scales would halve the waves (13.7 us
-// against 15.3 at 4999 x 8160, groups of 32, 13 vectors), and so would more
-// than 16 vectors.
+// The workgroup's shape.  Two tiles of rows a workgroup halve what x costs
+// and two tiles of vectors what W's operands cost, as long as every CU still
+// gets a workgroup (40.7 us against 49.7 with one tile of rows at 8192 x
+// 28672, 16 vectors, but 10.2 against 8.7 at 4096 x 8192; 15.6 us against
+// 18.6 with two blocks of 16 vectors at 8192 x 8192, 32 vectors, but 7.5
+// against 6.4 at 4096 x 4096).  16 waves with blocks of 128 columns hide
+// more of each other's waits than 8 with 256 (11.5 us against 12.8 at 8192 x
+// 8192, 16 vectors; 8.7 against 9.7 at 4096 x 8192), but long rows in many
+// workgroups want whole 128-byte lines of W (40.7 us against 47.3 at 8192 x
+// 28672; 27.2 against 30.3 at 5000 x 28672).
 template <bool BF16, int GS, bool ZP>
 bool launch_shape(const lt::Mv4Params &P, hipStream_t s) {
-  constexpr int S = GS == 4 ? 256 : 128;
-  if (P.batch > 32) return launch_tiles<BF16, 4, 2, GS, ZP, 4, 64, 128>(P, s);
-  if (P.batch > 16) return launch_tiles<BF16, 2, 2, GS, ZP, 8, 32, 128>(P, s);
-  if (P.rows > 4096) {
-    if (P.batch > 8) return launch_tiles<BF16, 1, 2, GS, ZP, 8, 16, S>(P, s);
-    if (P.batch > 4) return launch_tiles<BF16, 1, 2, GS, ZP, 8, 8, S>(P, s);
-    return launch_tiles<BF16, 1, 2, GS, ZP, 8, 4, S>(P, s);
-  }
-  if (P.batch > 8) return launch_tiles<BF16, 1, 1, GS, ZP, 8, 16, S>(P, s);
-  return launch_tiles<BF16, 1, 1, GS, ZP, 8, 8, S>(P, s);
+  const bool lines = P.cols > 16384;
+  if (P.batch > 16 && (uint64_t)P.rows * ((P.batch + 31) / 32) > 4096)
+    return launch_tiles<BF16, 2, 2, GS, ZP, 8, 32, 128>(P, s);
+  if ((uint64_t)P.rows * ((P.batch + 15) / 16) <= 4096)
+    return P.batch > 8 ? launch_tiles<BF16, 1, 1, GS, ZP, 16, 16, 128>(P, s)
+                       : launch_tiles<BF16, 1, 1, GS, ZP, 16, 8, 128>(P, s);
+  if (P.batch > 8)
+    return lines ? launch_tiles<BF16, 1, 2, GS, ZP, 8, 16, 256>(P, s) : launch_tiles<BF16, 1, 2, GS, ZP, 16, 16, 128>(P, s);
+  if (P.batch > 4)
+    return lines ? launch_tiles<BF16, 1, 2, GS, ZP, 8, 8, 256>(P, s) : launch_tiles<BF16, 1, 2, GS, ZP, 16, 8, 128>(P, s);
+  return lines ? launch_tiles<BF16, 1, 2, GS, ZP, 8, 4, 256>(P, s) : launch_tiles<BF16, 1, 2, GS, ZP, 16, 4, 128>(P, s);
 }
 
 template <bool BF16, bool ZP>

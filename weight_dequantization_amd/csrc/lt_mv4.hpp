@@ -183,7 +183,7 @@ __device__ __forceinline__ void mv4_transpose(uint32_t d[4]) {
 }
 
 // The matrix-core form.  The workgroup's NW waves share RT tiles of 16 rows of
-// W and take blocks of 256 columns in turn.  A wave loads its block of W and
+// W and take blocks of S columns in turn.  A wave loads its block of W and
 // of x with neighbouring lanes side by side in memory and turns both in its
 // own part of LDS to operand order: lane (n, g) = (lane % 16, lane / 16) holds
 // 32 codes of row n, columns 32 g .. + 31 of each half block, and vector n's
@@ -211,7 +211,11 @@ __global__ void __launch_bounds__(64 * NW) mv4_kernel(Mv4Params P) {
   const uint32_t nblk = (P.cols + S - 1) / S;
   const uint32_t gc = P.group < P.cols ? (uint32_t)P.group : P.cols;   // columns of a row that share a scale
   const bool run = GPI == 1 || gc == 32 * GS;                          // a block's groups follow one another
-  const uint32_t r0 = blockIdx.x * (RT * 16);
+  // blocks of rows in turn over the 8 L2s; the blocks of vectors of the same rows follow on the same one
+  const uint32_t vblocks = (P.batch + XR - 1) / XR;
+  const uint32_t pass = blockIdx.x / (8 * vblocks), in_pass = blockIdx.x % (8 * vblocks);
+  const uint32_t r0 = (pass * 8 + in_pass % 8) * (RT * 16), v0 = in_pass / 8 * XR;
+  if (r0 >= P.rows) return;
   const uint8_t *wp[WI];                     // rows of this lane's loads
 #pragma unroll
   for (int i = 0; i < WI; i++) {
@@ -228,8 +232,8 @@ __global__ void __launch_bounds__(64 * NW) mv4_kernel(Mv4Params P) {
 #pragma unroll
   for (int i = 0; i < XI; i++) {
     const uint32_t b = i * (64 / CX) + lane / CX;
-    xon[i] = b < P.batch && b < XR;
-    xp[i] = P.x + (xon[i] ? b : 0) * P.x_stride + 8 * (lane % CX);
+    xon[i] = v0 + b < P.batch && b < XR;
+    xp[i] = P.x + (xon[i] ? v0 + b : 0) * P.x_stride + 8 * (lane % CX);
   }
   auto turn = [](uint32_t r) { return CW == 8 ? r & 7u : (r >> 2) & 3u; };
   const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -350,8 +354,8 @@ __global__ void __launch_bounds__(64 * NW) mv4_kernel(Mv4Params P) {
   __syncthreads();
   for (uint32_t k = threadIdx.x; k < RT * MT * 256; k += 64 * NW) {
     const uint32_t l = k & 63u, i = (k >> 6) & 3u, mt = (k >> 8) % MT, rt = (k >> 8) / MT;
-    const uint32_t b = mt * 16 + 4 * (l >> 4) + i, r = r0 + rt * 16 + (l & 15u);
-    if (b >= P.batch || r >= P.rows) continue;
+    const uint32_t b = v0 + mt * 16 + 4 * (l >> 4) + i, r = r0 + rt * 16 + (l & 15u);
+    if (b >= P.batch || b >= v0 + XR || r >= P.rows) continue;
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; w++) v += red[w * RT * MT * 256 + k];

@@ -60,10 +60,11 @@ Plan plan_of(const lt::Kv4View &C, const lt::Kv4Rows &B, uint64_t max_q, uint64_
              uint32_t window, uint32_t sinks) {
   Plan p;
   const uint64_t rows = max_q * ratio;
-  p.wide = rows > (C.dim == 256 ? 16 : 32);
-  p.nt = C.dim == 256 || rows <= 16 || (p.wide && rows <= 64) ? 1 : 2;
-  p.unit = 16 * p.nt;
-  p.row_blocks = (uint32_t)((rows + p.unit * (p.wide ? 4 : 1) - 1) / (p.unit * (p.wide ? 4 : 1)));
+  // Up to 32 rows share a workgroup's tiles among its waves; more give each
+  // wave rows of its own (8 kv heads of 128, 4000 tokens, 8 sequences: 32 rows
+  // 25 us against 37, 40 rows 33 against 41; heads of 256, 32 rows: 40 against
+  // 61).
+  p.wide = rows > 32;
   // the most tiles a row sees, and the workgroups without a split
   uint64_t tiles = (max_kv + 31) / 32;
   if (window) {
@@ -71,12 +72,31 @@ Plan plan_of(const lt::Kv4View &C, const lt::Kv4Rows &B, uint64_t max_q, uint64_
     tiles = kept < tiles ? kept : tiles;
   }
   if (tiles < 1) tiles = 1;
+  // One tile of 16 rows a wave where two would be half empty, or leave the
+  // CUs too little to do (2 sequences of 100 tokens of 1000: 30 us against 39;
+  // 8 sequences of 16 tokens of 4000: 59 against 53), or not fit registers.
+  auto blocks = [&](uint64_t unit) { return (rows + unit - 1) / unit; };
+  const uint64_t work = (uint64_t)B.n_seqs * C.kv_heads * blocks(128) * tiles;
+  p.nt = C.dim == 256 || rows <= 16 || (p.wide && (rows <= 64 || work < 15 * 256)) ? 1 : 2;
+  p.unit = 16 * p.nt;
+  p.row_blocks = (uint32_t)blocks(p.unit * (p.wide ? 4 : 1));
   const uint64_t units = (uint64_t)B.n_seqs * C.kv_heads * p.row_blocks;
   uint64_t chunk = tiles;
+  // Chunks so that the workgroups fill the CUs: 2 a CU (one token of 131071:
+  // 35 us, with 1 a CU 38, with 4 41), or 1 where registers allow no more (8
+  // sequences of 4000, 32 rows, groups of 32: 29 us against 37); at least 16 tiles, below
+  // which the join costs more than it saves (one token of 16000: 12.7 us
+  // against 14.3 with 8), and at most 128, so that ragged lengths even out (one
+  // sequence of 100000 among 63 of 500: 90 us against 651).
+  // Rows on their own waves are split only when few workgroups would run, and
+  // less when there are more, as they have more to join (16 tokens of 2000:
+  // 27 us, unsplit 42; 2 sequences of 100 tokens of 1000: 39 us against 44).
   if (p.wide) {
-    if (units < 256) chunk = (units * tiles + 511) / 512 < 32 ? 32 : (units * tiles + 511) / 512;
+    const uint32_t least = units <= 64 ? 16 : 32;
+    chunk = units >= 256 ? tiles : (units * tiles + 511) / 512 < least ? least : (units * tiles + 511) / 512;
   } else if (tiles > 16) {
-    chunk = (units * tiles + 511) / 512;
+    const uint32_t fill = C.dim == 256 || (C.dim == 128 && p.nt == 2 && C.group == 32) ? 256 : 512;
+    chunk = (units * tiles + fill - 1) / fill;
     chunk = chunk < 16 ? 16 : chunk > 128 ? 128 : chunk;
   }
   p.chunk_shift = 0;

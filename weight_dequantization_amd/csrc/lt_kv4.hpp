@@ -8,11 +8,6 @@
 
 namespace lt {
 
-template <int V>
-struct kv4_set {
-  static constexpr int value = V;
-};
-
 struct Kv4View {
   uint8_t *pages;
   uint64_t n_pages;
@@ -534,14 +529,23 @@ __device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over 
 // the largest value scale so far would pass 2^15, and is then set so that it
 // is 2^7 (fp16 keeps 11 bits down to 2^-14).
 //
-// WIDE: the 4 waves of a workgroup take different rows and every tile (one
-// wave a workgroup: 751 us for prompt chunks against 721, they share what
-// they load).  Otherwise they share rows, take every 4th tile and join their
-// sums.
-// waves of a SIMD that the registers leave room for
+// WIDE: the 4 waves of a workgroup take different rows and every tile, and
+// meet the same lines in their L1.  Otherwise they share rows, take every 4th
+// tile and join their sums through LDS.
+//
+// Bounds.  Few rows: bytes in flight.  A tile of 32 tokens of one head is 4 to
+// 9 KB that one wave waits for once a step; 64 ragged sequences read 3.4 TB/s
+// (112 us at 6.1 TB/s, 143 here), one token of 131071 3.6 (25 us, 31).  Many
+// rows: VALU operations, which unpack codes and make weights while the matrix
+// cores wait (prompt chunks: 737 TFLOP/s, 62% of what large products reach;
+// VALU busy 68% of the time).
+
+// waves of a SIMD that the registers leave room for (groups of 32 of 128
+// values spill with two; 4 sequences a head of 8, 64 sequences of 1000, groups
+// of 64: 25.7 us with two, 37.4 with one)
 template <int D, int G, int NT, bool WIDE>
 constexpr int kv4_waves() {
-  return D == 256 || (D == 128 && NT == 2 && (G == 32 || !WIDE)) ? 1 : 2;
+  return D == 256 || (D == 128 && NT == 2 && G == 32) ? 1 : 2;
 }
 
 template <int D, int G, int NT, bool WIDE>
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   constexpr int JOIN = VH * 4 < 8 ? VH * 4 : 8;       // of them joined at a time
   __shared__ kv4_f4 join_o[WIDE ? 1 : 4][WIDE ? 1 : JOIN][64];
   __shared__ float join_ml[WIDE ? 1 : 4][WIDE ? 1 : NT][2][16];
-  __shared__ __attribute__((aligned(16))) uint32_t scale_lds[4][2][NG][64];
+  __shared__ __attribute__((aligned(16))) uint32_t scale_lds[4][NG][64];
   const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // late rows see the most tokens: they start first
@@ -589,10 +593,7 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   // read.  Codes come as operands; a tile's scales come once, dword k of lanes
   // 0..31 for its keys in group k, of lanes 32..63 for its values, and go
   // through the wave's part of LDS to the lanes that need 4 tokens' each.
-  // Where registers allow, two sets of them: loads are on their way two steps
-  // before their use (64 ragged sequences: 166 us with one set, 151 with two).
-  constexpr int SETS = WIDE || D == 256 || (D == 128 && G == 32) ? 1 : 2;
-  uint32_t kd[SETS][2][KC], vd[SETS][2][2 * VH], sr[SETS][NG], ks[2][NG][4], vs[2][NG][4];
+  uint32_t kd[2][KC], vd[2][2 * VH], sr[NG], ks[2][NG][4], vs[2][NG][4];
   const uint32_t ps = C.page_shift, n_pages = (uint32_t)C.n_pages;
   uint8_t *head0 = C.pages + (uint64_t)h * ((uint32_t)(D + 8 * NG) << ps);
   const uint32_t k_at = n * (D / 2) + g * (D / 8), v_at = lane * (D / 8);
@@ -602,44 +603,40 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
     const uint64_t at = (uint64_t)((uint32_t)page < n_pages ? (uint32_t)page : 0u) * C.kv_heads * bytes;
     return __builtin_amdgcn_make_buffer_rsrc(head0 + at, 0, (int)bytes, 0x00020000);
   };
-  auto load_keys = [&](auto set, uint32_t j0, int32_t page) {   // and the scales of both
-    constexpr int S = decltype(set)::value;
+  auto load_keys = [&](uint32_t j0, int32_t page) {   // and the scales of both
     const uint32_t slot = j0 & ((1u << ps) - 1);
     const auto blk = block_of(page);
 #pragma unroll
-    for (int u = 0; u < 2; u++) kv4_load(kd[S][u], blk, k_at + 16 * u * (D / 2), slot * (D / 2));
+    for (int u = 0; u < 2; u++) kv4_load(kd[u], blk, k_at + 16 * u * (D / 2), slot * (D / 2));
 #pragma unroll
     for (int k = 0; k < NG; k++)
-      sr[S][k] = __builtin_amdgcn_raw_buffer_load_b32(blk, s_at, ((uint32_t)(D / 2 + 4 * k) << ps) + slot * 4, 0);
+      sr[k] = __builtin_amdgcn_raw_buffer_load_b32(blk, s_at, ((uint32_t)(D / 2 + 4 * k) << ps) + slot * 4, 0);
   };
-  auto load_values = [&](auto set, uint32_t j0, int32_t page) {
-    constexpr int S = decltype(set)::value;
+  auto load_values = [&](uint32_t j0, int32_t page) {
     const uint32_t slot = j0 & ((1u << ps) - 1);
     const auto blk = block_of(page);
 #pragma unroll
     for (int u = 0; u < 2; u++)
-      kv4_load(vd[S][u], blk, v_at + 16 * u * (D / 2), ((uint32_t)(D / 2 + 4 * NG) << ps) + slot * (D / 2));
+      kv4_load(vd[u], blk, v_at + 16 * u * (D / 2), ((uint32_t)(D / 2 + 4 * NG) << ps) + slot * (D / 2));
   };
   uint32_t s_most = 0;                               // the lane's largest value scale of the tile to come
-  auto put_scales = [&](auto set) {
-    constexpr int S = decltype(set)::value;
+  auto put_scales = [&]() {
     s_most = 0;
     wave_order();
 #pragma unroll
     for (int k = 0; k < NG; k++) {
-      scale_lds[wave][S][k][lane] = sr[S][k];
-      const uint32_t b = lane < 32 ? 0 : sr[S][k] & 0x7FFFu;
+      scale_lds[wave][k][lane] = sr[k];
+      const uint32_t b = lane < 32 ? 0 : sr[k] & 0x7FFFu;
       s_most = s_most > b ? s_most : b;
     }
     wave_order();
   };
-  auto get_scales = [&](auto set, bool value) {
-    constexpr int S = decltype(set)::value;
+  auto get_scales = [&](bool value) {
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
       for (int k = 0; k < NG; k++) {
-        const kv4_u4 v = *(const kv4_u4 *)&scale_lds[wave][S][k][(value ? 32 : 0) + 16 * u + 4 * g];
+        const kv4_u4 v = *(const kv4_u4 *)&scale_lds[wave][k][(value ? 32 : 0) + 16 * u + 4 * g];
 #pragma unroll
         for (int q = 0; q < 4; q++) (value ? vs[u][k][q] : ks[u][k][q]) = v[q];
       }
@@ -651,14 +648,8 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   auto tile_of = [&](uint32_t k) { return first_of(k < i1 ? k : i); };   // past the end: loads that nothing uses
   uint32_t j0 = first_of(i), j1 = tile_of(i + STRIDE), j2 = tile_of(i + 2 * STRIDE), j3 = tile_of(i + 3 * STRIDE);
   int32_t page0 = page_of(j0), page1 = page_of(j1), page2 = page_of(j2), page3 = page_of(j3);
-  const kv4_set<0> even;
-  const kv4_set<SETS - 1> uneven;
-  load_keys(even, j0, page0);
-  load_values(even, j0, page0);
-  if (SETS == 2) {
-    load_keys(uneven, j1, page1);
-    load_values(uneven, j1, page1);
-  }
+  load_keys(j0, page0);
+  load_values(j0, page0);
 
   // the rows' queries, limits and softmax state
   kv4_h8 qf[NT][KC];
@@ -741,13 +732,12 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   // K's products with the queries, and the scores out of them
   kv4_f4 acc[NT][2][NG];
   float x[NT][8];
-  auto products = [&](auto set) {
-    constexpr int S = decltype(set)::value;
+  auto products = [&]() {
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
       for (int c = 0; c < KC; c++) {
-        const uint32_t w = kd[S][u][c], w8 = w >> 8;
+        const uint32_t w = kd[u][c], w8 = w >> 8;
         const kv4_u4 a = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
@@ -809,15 +799,14 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   // values, the next tile's scores are multiplied, and each register's next
   // load is on its way as soon as it has been used.
   if (i < i1) {
-    put_scales(even);
-    products(even);
-    get_scales(even, false);
-    get_scales(even, true);
-    load_keys(even, SETS == 2 ? j2 : j1, SETS == 2 ? page2 : page1);
+    put_scales();
+    products();
+    get_scales(false);
+    get_scales(true);
+    load_keys(j1, page1);
     scores();
-    // `own` holds the tile's values, `other` the next tile's keys
-    auto step = [&](auto own, auto other) {
-      constexpr int S = decltype(own)::value;
+    // the registers hold the tile's values and the next tile's keys
+    auto step = [&]() {
       const uint32_t j4 = tile_of(i + 4 * STRIDE);
       const int32_t page4 = page_of(j4);
       const bool bad = (uint32_t)page0 >= n_pages;
@@ -890,18 +879,18 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
             rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, w), one, rs[nt][k], false);
           }
         }
-      put_scales(other);
-      get_scales(other, true);
-      get_scales(other, false);
-      products(other);
-      load_keys(other, SETS == 2 ? j3 : j2, SETS == 2 ? page3 : page2);
+      put_scales();
+      get_scales(true);
+      get_scales(false);
+      products();
+      load_keys(j2, page2);
 #pragma unroll
       for (int hh = 0; hh < VH; hh++)
 #pragma unroll
         for (int k = 0; k < 4; k++) {
           const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu;
-          const kv4_u4 a = {(vd[S][0][2 * hh] >> sh) & m4, (vd[S][0][2 * hh + 1] >> sh) & m4,
-                            (vd[S][1][2 * hh] >> sh) & m4, (vd[S][1][2 * hh + 1] >> sh) & m4};
+          const kv4_u4 a = {(vd[0][2 * hh] >> sh) & m4, (vd[0][2 * hh + 1] >> sh) & m4,
+                            (vd[1][2 * hh] >> sh) & m4, (vd[1][2 * hh + 1] >> sh) & m4};
           const int grp = (64 * hh + 16 * k) / G;
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
@@ -910,32 +899,13 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
                                                                   __builtin_bit_cast(kv4_h8, pb), o[nt][hh][k], 0, 0, 0);
           }
         }
-      load_values(own, SETS == 2 ? j2 : j1, SETS == 2 ? page2 : page1);
+      load_values(j1, page1);
       scores();
-      if constexpr (!WIDE) {
-        // products spread between the other operations (64 ragged sequences:
-        // 171 us as the compiler orders them, 160 so; no gain where VALU
-        // operations fill the time)
-#pragma unroll
-        for (int t = 0; t < NT * (2 * KC + 4 * VH); t++) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
-        }
-      }
       i += STRIDE;
       j0 = j1, j1 = j2, j2 = j3, j3 = j4;
       page0 = page1, page1 = page2, page2 = page3, page3 = page4;
     };
-    const uint32_t steps = (i1 - i + STRIDE - 1) / STRIDE;
-    if constexpr (SETS == 2) {
-      for (uint32_t k = steps / 2; k > 0; k--) {
-        step(even, uneven);
-        step(uneven, even);
-      }
-      if (steps & 1) step(even, uneven);
-    } else {
-      for (uint32_t k = steps; k > 0; k--) step(even, even);
-    }
+    for (uint32_t k = (i1 - i + STRIDE - 1) / STRIDE; k > 0; k--) step();
   }
 
   // row sums over the 4 lanes of a row; outputs without their offsets

@@ -501,3 +501,26 @@ def test_offsets_past_32_bits():
     for a, b in zip(*outs):
         assert torch.equal(a, b)
     assert torch.all((outs[0][0] - k).abs() < 0.3)
+
+
+@pytest.mark.parametrize("new,heads,dtype", [(1, 8, F16), (1, 16, F16), (1, 8, BF16), (3, 8, F16), (8192, 4, F16)])
+def test_long_sums_keep_their_precision(new, heads, dtype):
+    """Over a long cache the output is small against the sums that make it.
+    Root mean squares instead of the worst case: every rounding to a type with
+    relative errors up to r is one of r / sqrt(3); roundings of weights are
+    independent, and uniform codes lie 4.61 steps from their mean; three times
+    that for what fp32 adds and for chance (128 dims)."""
+    n, D = 33000, 128
+    c = Case([new], [n], P=64, H=1, D=D)
+    q, out, _ = run_attention(c, dtype, heads)
+    k, v, sv = c.seq(0, 0)
+    for t, h in ((0, 0), (new - 1, heads - 1)):
+        m = n - new + t + 1
+        x = D ** -0.5 * (k[:m] @ q[t, h].double().cpu().numpy())
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        o = w @ v[:m]
+        off = out[t, h].double().cpu().numpy() - o
+        weights = 2.0 ** -11 * np.sqrt((w ** 2) @ (4.61 * sv[:m]) ** 2)
+        limit = 3 * np.sqrt(np.mean(weights ** 2 + (HALF[dtype] * o) ** 2) / 3)
+        assert np.sqrt(np.mean(off ** 2)) <= limit, (t, h, np.sqrt(np.mean(off ** 2)) / limit)

@@ -128,9 +128,9 @@ void launch_read(dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Ro
   }
 }
 
-template <int D, int G, int NT, bool WIDE>
+template <int D, int G, int NT, bool WIDE, bool REST>
 void launch_rows(dim3 grid, hipStream_t s, const lt::Kv4View &C, const lt::Kv4Rows &B, const lt::Kv4Attn &A) {
-  hipLaunchKernelGGL((lt::kv4_attention_kernel<D, G, NT, WIDE>), grid, dim3(256), 0, s, C, B, A);
+  hipLaunchKernelGGL((lt::kv4_attention_kernel<D, G, NT, WIDE, REST>), grid, dim3(256), 0, s, C, B, A);
 }
 
 template <int D, int G>
@@ -138,9 +138,12 @@ void launch_attention(const Plan &p, dim3 grid, hipStream_t s, const lt::Kv4View
                       const lt::Kv4Attn &A) {
   constexpr int NT = D == 256 ? 1 : 2;   // more than 16 rows of 256 values do not fit a wave's registers
   if (p.wide) {
-    p.nt == 1 ? launch_rows<D, G, 1, true>(grid, s, C, B, A) : launch_rows<D, G, NT, true>(grid, s, C, B, A);
+    p.nt == 1 ? launch_rows<D, G, 1, true, false>(grid, s, C, B, A) : launch_rows<D, G, NT, true, false>(grid, s, C, B, A);
+  } else if (p.nt == 1) {
+    const bool rest = !A.bf16 && (uint64_t)A.max_q * A.ratio <= 8;
+    rest ? launch_rows<D, G, 1, false, true>(grid, s, C, B, A) : launch_rows<D, G, 1, false, false>(grid, s, C, B, A);
   } else {
-    p.nt == 1 ? launch_rows<D, G, 1, false>(grid, s, C, B, A) : launch_rows<D, G, NT, false>(grid, s, C, B, A);
+    launch_rows<D, G, NT, false, false>(grid, s, C, B, A);
   }
   if (p.splits > 1)
     hipLaunchKernelGGL((lt::kv4_join_kernel<D>), dim3(A.heads, A.max_q, B.n_seqs), dim3(256), 0, s, B, A, p.unit);

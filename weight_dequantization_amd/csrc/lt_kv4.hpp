@@ -522,8 +522,18 @@ __device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over 
 // came out; operand A has dims 64 h + 16 k + n of the step's tokens from one
 // load, unpacked like K's.  The value scales go onto the weights: p' = p s,
 // rounded to fp16 here and only here; what rounding does to the mean code is
-// kept out by taking codes from 8 on: sum p v = sum p' (c - 8) + sum p (m + 8 s),
-// with sum p' of the rounded weights.
+// kept out by taking codes from 7.5 on: sum p v = sum p' (c - 7.5) + sum p (m
+// + 7.5 s), with sums of the rounded weights.  So that a long sum of codes of
+// one sign does not outgrow its small result in fp32, every second token
+// counts its code down, 15 - c, with a negative weight, and the sum of p' is
+// taken with the same signs.
+//
+// REST, for fp16 outputs of 8 rows or fewer: the other 8 columns of B would
+// idle; they hold the same rows, and what p' lost in its rounding (relative
+// error for one token of 131071, of which the rounding of the output is
+// 2.0e-4: 8.0e-4 without signs, 3.3e-4 with them, 2.6e-4 with both; 39.0 us
+// against 36.7).  A bf16 output is rounded 8 times as coarsely (1.7e-3 either
+// way; 64 ragged sequences: 160 us against 150).
 //
 // Running softmax: weights are 2^(x - ref); ref moves only when a weight times
 // the largest value scale so far would pass 2^15, and is then set so that it
@@ -543,13 +553,14 @@ __device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over 
 // waves of a SIMD that the registers leave room for (groups of 32 of 128
 // values spill with two; 4 sequences a head of 8, 64 sequences of 1000, groups
 // of 64: 25.7 us with two, 37.4 with one)
-template <int D, int G, int NT, bool WIDE>
+template <int D, int G, int NT>
 constexpr int kv4_waves() {
   return D == 256 || (D == 128 && NT == 2 && G == 32) ? 1 : 2;
 }
 
-template <int D, int G, int NT, bool WIDE>
-__global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attention_kernel(Kv4View C, Kv4Rows B, Kv4Attn A) {
+template <int D, int G, int NT, bool WIDE, bool REST>
+__global__ void __launch_bounds__(256, (kv4_waves<D, G, NT>())) kv4_attention_kernel(Kv4View C, Kv4Rows B, Kv4Attn A) {
+  static_assert(!REST || (NT == 1 && !WIDE), "8 rows fill half a tile");
   constexpr int NG = D / G, KC = D / 32, VH = D / 64;
   constexpr int CPG = G / 32;                        // score products of a group
   constexpr int VALS = NT * VH * 4;                  // output registers of 4
@@ -658,7 +669,7 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
   kv4_f4 o[NT][VH][4];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    uint32_t r = row0 + nt * 16 + n;
+    uint32_t r = row0 + nt * 16 + (REST ? n & 7u : n);
     r = r < rows ? r : rows - 1;
     const uint32_t t = r / A.ratio, hd = h * A.ratio + (r - t * A.ratio);
     const int32_t p = p_base + (int32_t)t;
@@ -869,11 +880,13 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
 #pragma unroll
         for (int t = 0; t < 8; t += 2) {
           const uint32_t sa = vs[t >> 2][k][t & 3], sb = vs[t >> 2][k][(t & 3) + 1];
-          const float ma = fmaf(8.0f, kv4_lo(sa), kv4_hi(sa)), mb = fmaf(8.0f, kv4_lo(sb), kv4_hi(sb));
+          const float ma = fmaf(7.5f, kv4_lo(sa), kv4_hi(sa)), mb = fmaf(7.5f, kv4_lo(sb), kv4_hi(sb));
           const kv4_h2 one = {(_Float16)1.0f, (_Float16)1.0f};
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            const uint32_t w = kv4_pair(p[nt][t] * kv4_lo(sa), p[nt][t + 1] * kv4_lo(sb));
+            const float wa = p[nt][t] * kv4_lo(sa), wb = p[nt][t + 1] * -kv4_lo(sb);
+            uint32_t w = kv4_pair(wa, wb);
+            if constexpr (REST) w = n & 8u ? kv4_pair(wa - kv4_lo(w), wb - kv4_hi(w)) : w;
             pf[nt][k][t >> 1] = w;
             off[nt][k] = fmaf(p[nt][t + 1], mb, fmaf(p[nt][t], ma, off[nt][k]));
             rs[nt][k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(kv4_h2, w), one, rs[nt][k], false);
@@ -888,9 +901,9 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
       for (int hh = 0; hh < VH; hh++)
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-          const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu;
-          const kv4_u4 a = {(vd[0][2 * hh] >> sh) & m4, (vd[0][2 * hh + 1] >> sh) & m4,
-                            (vd[1][2 * hh] >> sh) & m4, (vd[1][2 * hh + 1] >> sh) & m4};
+          const uint32_t sh = k >= 2 ? 8 : 0, m4 = k & 1 ? 0x00F000F0u : 0x000F000Fu, flip = 0x00FF0000u;
+          const kv4_u4 a = {(vd[0][2 * hh] >> sh ^ flip) & m4, (vd[0][2 * hh + 1] >> sh ^ flip) & m4,
+                            (vd[1][2 * hh] >> sh ^ flip) & m4, (vd[1][2 * hh + 1] >> sh ^ flip) & m4};
           const int grp = (64 * hh + 16 * k) / G;
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
@@ -908,12 +921,28 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT, WIDE>())) kv4_attent
     for (uint32_t k = (i1 - i + STRIDE - 1) / STRIDE; k > 0; k--) step();
   }
 
+  if constexpr (REST) {   // of rows 0..7, what the rounded weights and what their rests give
+    auto both = [](float v) {
+      return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
+    };
+#pragma unroll
+    for (int k = 0; k < NG; k++) rs[0][k] = both(rs[0][k]);
+#pragma unroll
+    for (int hh = 0; hh < VH; hh++)
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const float v = o[0][hh][k][q];
+          o[0][hh][k][q] = both(v);
+        }
+  }
   // row sums over the 4 lanes of a row; outputs without their offsets
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
     l[nt] = kv4_over_groups(l[nt], false);
 #pragma unroll
-    for (int k = 0; k < NG; k++) off[nt][k] = kv4_over_groups(fmaf(-8.0f, rs[nt][k], off[nt][k]), false);
+    for (int k = 0; k < NG; k++) off[nt][k] = kv4_over_groups(fmaf(-7.5f, rs[nt][k], off[nt][k]), false);
 #pragma unroll
     for (int hh = 0; hh < VH; hh++)
 #pragma unroll

@@ -96,7 +96,9 @@ __device__ __forceinline__ void store8(uint16_t *p, bool bf16, const float v[8])
 // tokens side by side) and its loads each fall together, and `heads_each`
 // heads of theirs one after another, for which a token's place and rotation
 // are fetched once.  The rotation's products and sums are rounded one by one
-// (no contraction), as its formula reads.
+// (no contraction), as its formula reads.  Bytes bound it: ragged prompts of
+// 48 heads take 44 us for 177 MB, 4.0 TB/s of the 5.1 that a copy reaches; 64
+// single tokens 5.7 us, the time of a launch and of one token's chain.
 template <int LV, bool BF16>
 __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View C, Kv4Rows B, Kv4NewRows N, uint32_t heads_each) {
   constexpr uint32_t TPW = 64 / LV, D = 8 * LV;
@@ -341,7 +343,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4View C, Kv4Rows B, Kv4
   // different tokens falls into few channels of an L2.  Workgroups go to the
   // 8 L2s in turn: block x takes tile x % 8 of 8 and a group of up to 4 heads,
   // so that all heads of a token are written from one L2 at about one time
-  // (XXX us with a head an L2, XXX so, for 16 prefixes).
+  // (16 prefixes: 132 us with a head an L2, 118 so; loads before stores then
+  // made it 101, 429 MB at 4.2 TB/s of the 5.1 that a copy reaches).
   const uint32_t per = C.kv_heads >= 4 ? 4 : C.kv_heads >= 2 ? 2 : 1;   // heads of a workgroup
   const uint32_t h = (blockIdx.x >> 3) * per + wave % per, seq = blockIdx.y;
   if (h >= C.kv_heads) return;
@@ -543,12 +546,12 @@ __device__ __forceinline__ float kv4_over_groups(float v, bool max) {   // over 
 // meet the same lines in their L1.  Otherwise they share rows, take every 4th
 // tile and join their sums through LDS.
 //
-// Bounds.  Few rows: bytes in flight.  A tile of 32 tokens of one head is 4 to
-// 9 KB that one wave waits for once a step; 64 ragged sequences read 3.4 TB/s
-// (112 us at 6.1 TB/s, 143 here), one token of 131071 3.6 (25 us, 31).  Many
-// rows: VALU operations, which unpack codes and make weights while the matrix
-// cores wait (prompt chunks: 737 TFLOP/s, 62% of what large products reach;
-// VALU busy 68% of the time).
+// Bounds.  Few rows: bytes in flight; a wave waits for a tile of 32 tokens of
+// one head (4 to 9 KB) once a step.  64 ragged sequences: 143 us for 675 MB,
+// 4.7 TB/s of the 6.1 that a plain read reaches; one token of 131071: 34 us for
+// 151 MB.  Many rows: VALU operations, which unpack codes and make weights
+// while the matrix cores wait; prompt chunks: 636 us for 451 GFLOP, 709 TFLOP/s
+// of the 1190 of large products, VALU busy about 70% of the time.
 
 // waves of a SIMD that the registers leave room for (groups of 32 of 128
 // values spill with two; 4 sequences a head of 8, 64 sequences of 1000, groups
@@ -1031,7 +1034,9 @@ __global__ void __launch_bounds__(256, (kv4_waves<D, G, NT>())) kv4_attention_ke
 }
 
 // Joins the splits of a row: one workgroup a row (head, token of its sequence,
-// sequence), D / 4 threads a split, 4 splits' loads at a time.
+// sequence), D / 4 threads a split, 4 splits' loads at a time.  The parts come
+// out of the last level's cache: latency bounds it (4.7 us for 64 heads of 64
+// splits, 7.7 us for 64 sequences of 64 heads and up to 4 splits).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4Rows B, Kv4Attn A, uint32_t unit) {
   constexpr uint32_t T = D / 4, S = 256 / T;

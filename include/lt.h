@@ -759,7 +759,9 @@ lt_status lt_kv4_read(const lt_kv4_cache *cache, const lt_kv4_batch *batch, void
  *              aligned, owned by the caller, needing no particular contents:
  *              long caches are split over workgroups and joined from it in a
  *              fixed order (results are the same bits on every call)
- * Scores, softmax and sums are fp32.
+ * Scores, softmax and sums are fp32; a weight times its value scale is rounded
+ * to fp16 once.  LT_ERR_UNSUPPORTED beyond 65535 heads or 2^31 - 1 rows of all
+ * heads.
  */
 lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch, const void *q,
                            int64_t q_token_stride, int64_t q_head_stride, uint32_t heads, lt_dtype type,

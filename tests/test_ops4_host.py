@@ -170,3 +170,11 @@ def test_binding_refuses_wrong_tensors():
         lt.gemv_int4(z(64, d=torch.uint8), z(1), None, (2, 64), 64, z(3, 64), y=z(3, 3))
     with pytest.raises(TypeError):
         lt.gemv_int4(z(64, d=torch.uint8), z(1), None, (2, 64), 64, z(3, 64, d=torch.float32))
+
+
+@pytest.mark.parametrize("b,kw", [
+    (dict(seqs=1 << 16), {}), ({}, dict(heads=65538)), (dict(tokens=1 << 30, q=1), dict(heads=8)),
+    (dict(q=(1 << 31) - 1), dict(heads=4))])
+def test_attention_beyond_its_grid(b, kw):
+    """Sizes that its launches could not index are refused, not cut."""
+    assert attention(cache(), batch(**b), **kw) == UNSUPPORTED

@@ -275,7 +275,8 @@ lt_status lt_kv4_attention(const lt_kv4_cache *cache, const lt_kv4_batch *batch,
   if (!(scale > -3.4e38f && scale < 3.4e38f)) return LT_ERR_INVALID_ARG;
   const Plan p = plan_of(C, B, batch->max_q_len, batch->max_kv_len, heads / C.kv_heads, window, sinks);
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return LT_ERR_INVALID_ARG;
-  if (heads > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 || (p.splits > 1 && batch->max_q_len > 65535) ||
+  // (rows enough to pass the join's grid, 65536 new tokens, are never split)
+  if (heads > 65535 || (uint64_t)p.row_blocks * p.splits > 65535 ||
       (uint64_t)B.n_tokens * heads > 0x7FFFFFFFull ||
       (uint64_t)batch->max_q_len * (heads / C.kv_heads) > 0x7FFFFFFFull)
     return LT_ERR_UNSUPPORTED;
